@@ -62,6 +62,14 @@ _SIGNATURES = {
                                _P, ctypes.c_size_t, _P]),
     "attn_out_proj": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P]),
     "attn_out_proj_bwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "attn_head_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "attn_head_ce": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, ctypes.c_size_t, _P]),
+    "attn_head_ce_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P,
+                              ctypes.c_size_t, _P]),
+    "attn_head_distill": (_I, [_P, _P, _P, _P, ctypes.c_float, _P, _P, _I, _I, _I, _I, _I, _P,
+                               ctypes.c_size_t, _P]),
+    "attn_head_distill_bwd": (_I, [_P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _I, _I, _I,
+                                   _I, _I, _I, _P, ctypes.c_size_t, _P]),
     "attn_workspace_bytes_gqa": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I]),
     "attn_get_status": (_I, [_P]),
     "attn_error_string": (ctypes.c_char_p, [_I]),
@@ -246,6 +254,44 @@ def attn_out_proj_bwd(dy, o, w_o, d_o, dw_o, B, T, C, H, D, stream=None) -> int:
     """d_o = dy W_o ([B, H, T, D]) and dw_o = dy^T o (float32)."""
     return int(_lib.attn_out_proj_bwd(_ptr(dy), _ptr(o), _ptr(w_o), _ptr(d_o), _ptr(dw_o), B, T,
                                       C, H, D, _stream(stream)))
+
+
+def attn_head_workspace_bytes(N, V, C, K, is_bwd) -> int:
+    """Workspace of the attn_head_* calls; K = 0 for attn_head_ce*."""
+    return int(_lib.attn_head_workspace_bytes(N, V, C, K, int(bool(is_bwd))))
+
+
+def attn_head_ce(x, w, target, loss, lse, N, V, C, workspace, ws_bytes, stream=None) -> int:
+    """Cross-entropy of softmax(x W^T) per row, logits never stored; negative
+    targets leave their rows out (see include/attn.h)."""
+    return int(_lib.attn_head_ce(_ptr(x), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse), N, V, C,
+                                 _ptr(workspace), int(ws_bytes), _stream(stream)))
+
+
+def attn_head_ce_bwd(x, w, target, lse, dloss, dlse, dx, dw, N, V, C, dw_dtype, workspace,
+                     ws_bytes, stream=None) -> int:
+    """dx and dw of attn_head_ce's loss and lse; dlse may be None."""
+    return int(_lib.attn_head_ce_bwd(_ptr(x), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss),
+                                     _ptr(dlse), _ptr(dx), _ptr(dw), N, V, C, dw_dtype,
+                                     _ptr(workspace), int(ws_bytes), _stream(stream)))
+
+
+def attn_head_distill(x, w, t_idx, t_logit, temperature, loss, lse, N, V, C, K, t_dtype,
+                      workspace, ws_bytes, stream=None) -> int:
+    """KL divergence per row of softmax(x W^T / temperature) from a teacher's K
+    entries, logits never stored; negative ids are absent entries."""
+    return int(_lib.attn_head_distill(_ptr(x), _ptr(w), _ptr(t_idx), _ptr(t_logit),
+                                      float(temperature), _ptr(loss), _ptr(lse), N, V, C, K,
+                                      t_dtype, _ptr(workspace), int(ws_bytes), _stream(stream)))
+
+
+def attn_head_distill_bwd(x, w, t_idx, t_logit, temperature, lse, dloss, dlse, dx, dw, N, V, C, K,
+                          t_dtype, dw_dtype, workspace, ws_bytes, stream=None) -> int:
+    """dx and dw of attn_head_distill's loss and lse; dlse may be None."""
+    return int(_lib.attn_head_distill_bwd(_ptr(x), _ptr(w), _ptr(t_idx), _ptr(t_logit),
+                                          float(temperature), _ptr(lse), _ptr(dloss), _ptr(dlse),
+                                          _ptr(dx), _ptr(dw), N, V, C, K, t_dtype, dw_dtype,
+                                          _ptr(workspace), int(ws_bytes), _stream(stream)))
 
 
 def attn_get_status(stream=None) -> int:

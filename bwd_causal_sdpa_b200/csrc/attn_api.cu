@@ -1073,3 +1073,6 @@ extern "C" int attn_bwd_noalloc(const void* q, const void* k, const void* v, con
 
 // The projections around the attention (tensor-core GEMMs).
 #include "proj_api.cuh"
+
+// The losses of the output head on logits that are never stored.
+#include "head_api.cuh"

@@ -1,0 +1,371 @@
+// head_api.cuh -- host side of the output head's losses (included at the end
+// of attn_api.cu, whose helpers it uses): checks, workspace plan, operand maps
+// and the entry points attn_head_* of include/attn.h.
+#pragma once
+
+#include <algorithm>
+
+#include "head_rows.cuh"
+
+namespace {
+
+// Vocabulary rows per piece of the backward: the dz buffer of a piece (two
+// are in use) takes up to 128 MiB, or 4096 columns when the rows are many
+// (shorter pieces would add into dx more often than their products are worth).
+constexpr size_t kDzBytes = (size_t)128 << 20;
+constexpr long kDzMinCols = 4096;
+
+struct HeadPlan {
+  int rows_pad = 0, piece = 0, pieces = 0, parts = 0;
+  size_t n_kept = 0, row_of = 0, pos = 0, xc = 0, ids = 0, share = 0, entropy = 0, flags = 0;
+  size_t part = 0, named = 0;     // forward
+  size_t dz[2] = {0, 0}, acc = 0; // backward
+  long acc_rows = 0;
+  size_t total = 0;
+};
+
+bool head_sizes_ok(int N, int V, int C, int K) {
+  if (N <= 0 || V <= 0 || C <= 0 || K < 0 || K > head100::kMaxNamed) return false;
+  if (C % 8 != 0 || C > (1 << 20) || N > (1 << 26) || V > (1 << 26)) return false;
+  const long tiles_n = N / 256 + 1, tiles_v = V / 256 + 1, tiles_c = C / 256 + 1;
+  // units of one launch: the largest pieces of all three products
+  return tiles_n * tiles_v < (1L << 28) && tiles_v * tiles_c < (1L << 28) &&
+         tiles_n * tiles_c < (1L << 22);
+}
+
+// K = 0: a single target per row (attn_head_ce), else teacher entries per row.
+HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
+  using namespace head100;
+  HeadPlan p;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = round_up(off + bytes);
+    return at;
+  };
+  p.rows_pad = (N + kTile - 1) / kTile * kTile;
+  p.n_kept = take(4);
+  p.row_of = take((size_t)p.rows_pad * 4);
+  p.pos = take((size_t)N * 4);
+  p.xc = take((size_t)p.rows_pad * C * 2);
+  if (K > 0) {
+    p.ids = take((size_t)N * K * 4);
+    p.share = take((size_t)N * K * 4);
+    p.flags = take((size_t)N * 4);
+    if (!bwd) p.entropy = take((size_t)N * 4);
+  }
+  if (!bwd) {
+    p.parts = 2 * ((V + kTile - 1) / kTile);
+    p.part = take((size_t)p.parts * p.rows_pad * sizeof(float2));
+    p.named = take((size_t)N * std::max(K, 1) * 4);
+    p.total = off;
+    return p;
+  }
+  const long v_pad = ((long)V + kTile - 1) / kTile * kTile;
+  long cols = (long)(kDzBytes / ((size_t)p.rows_pad * 2)) / kTile * kTile;
+  cols = std::min(v_pad, std::max(cols, kDzMinCols));
+  p.pieces = (int)((V + cols - 1) / cols);
+  p.piece = (int)(((V + p.pieces - 1) / p.pieces + kTile - 1) / kTile * kTile);
+  p.pieces = (V + p.piece - 1) / p.piece;
+  for (int b = 0; b < std::min(p.pieces, 2); ++b)
+    p.dz[b] = take((size_t)p.rows_pad * p.piece * 2);
+  // the accumulators of dx: the most rows that any number of kept rows takes
+  const int tn = (C + kTile - 1) / kTile, kb = (std::min(p.piece, V) + kKB - 1) / kKB;
+  long rows = p.rows_pad;
+  for (int tm = 1; tm * kTile <= p.rows_pad && tm * tn < kPairs; ++tm) {
+    int splits, per;
+    split_dx(tm * tn, kb, splits, per);
+    rows = std::max(rows, (long)tm * kTile * splits);
+  }
+  p.acc_rows = rows;
+  p.acc = take((size_t)rows * C * 4);
+  p.total = off;
+  return p;
+}
+
+// A matrix [rows][cols] (row pitch `pitch` elements) in boxes of 128 bytes x
+// box_rows rows, 128-byte swizzle; past the edges reads give zeros, writes are
+// dropped.
+bool head_map(CUtensorMap* m, const void* base, bool f32, long rows, long cols, long pitch,
+              int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const int es = f32 ? 4 : 2;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)pitch * es};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same matrix in 64-column blocks, two of them (64 rows each) per box:
+// [cols / 64][rows][64]. A box of 128 rows of 128 bytes moves faster than two
+// of 64. cols % 64 == 0.
+bool head_block_map(CUtensorMap* m, const void* base, long rows, long cols) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(cols / 64)};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)head100::kKB, 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Everything the entry points share: arguments as the caller gave them.
+struct HeadCall {
+  const void *x, *w;
+  const int32_t* target;         // attn_head_ce*
+  const int32_t* t_idx;          // attn_head_distill*
+  const void* t_logit;
+  float tau;
+  int t_dtype;
+  float *loss, *lse_out;         // forward
+  const float *lse, *dloss, *dlse;  // backward
+  void *dx, *dw;
+  int dw_dtype;
+  int N, V, C, K;
+  bool bwd;
+};
+
+int head_check(const HeadCall& c, void* ws, size_t ws_bytes) {
+  if (!c.x || !c.w) return ATTN_EINVAL;
+  if (c.K == 0 ? !c.target : (!c.t_idx || !c.t_logit)) return ATTN_EINVAL;
+  if (c.bwd ? (!c.lse || !c.dloss || !c.dx || !c.dw) : (!c.loss || !c.lse_out)) return ATTN_EINVAL;
+  if (c.N <= 0 || c.V <= 0 || c.C <= 0) return ATTN_EINVAL;
+  if (!(c.tau > 0.f) || !isfinite(c.tau) || !isfinite(1.f / c.tau)) return ATTN_EINVAL;
+  if (c.t_dtype != ATTN_BF16 && c.t_dtype != ATTN_F32) return ATTN_EINVAL;
+  if (c.dw_dtype != ATTN_BF16 && c.dw_dtype != ATTN_F32) return ATTN_EINVAL;
+  if (!head_sizes_ok(c.N, c.V, c.C, c.K)) return ATTN_EUNSUPPORTED;
+  if (!aligned(c.x, 16) || !aligned(c.w, 16) || !aligned(c.target, 4) || !aligned(c.t_idx, 4) ||
+      !aligned(c.t_logit, c.t_dtype == ATTN_F32 ? 4 : 2) || !aligned(c.loss, 4) ||
+      !aligned(c.lse_out, 4) || !aligned(c.lse, 4) || !aligned(c.dloss, 4) ||
+      !aligned(c.dlse, 4) || !aligned(c.dx, 16) || !aligned(c.dw, 16))
+    return ATTN_EALIGN;
+  if (!ws || ws_bytes < head_plan(c.N, c.V, c.C, c.K, c.bwd).total) return ATTN_EWORKSPACE;
+  if (!aligned(ws, 16)) return ATTN_EALIGN;
+  return ATTN_OK;
+}
+
+int head_gemm(const head100::Maps& maps, const head100::Params& p, cudaStream_t st) {
+  using namespace head100;
+  static bool smem_done[64];
+  if (!ensure_smem(head_gemm_kernel, kSmAlloc, smem_done)) return ATTN_ECUDA;
+  long units = 0;
+  for (int j = 0; j < p.n_jobs; ++j) units += job_dims(p.job[j], p.N, p.C, p.kb_first).units;
+  // fewer kept rows may mean more parts of dx, never more than two per pair
+  for (int j = 0; j < p.n_jobs; ++j)
+    if (p.job[j].kind == JOB_DX) units = std::max<long>(units, kPairs);
+  const unsigned pairs = (unsigned)std::min<long>(units, kPairs);
+  ATTN_LAUNCH(KK_HEAD_GEMM, st, pdl_cluster_launch(head_gemm_kernel, dim3(2 * pairs), kThreads,
+                                                   kSmAlloc, st, 2u, maps, p));
+  return launch_status();
+}
+
+int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) {
+  using namespace head100;
+  if (int rc = head_check(c, workspace, ws_bytes)) return rc;
+  const HeadPlan hp = head_plan(c.N, c.V, c.C, c.K, c.bwd);
+  cudaStream_t st = (cudaStream_t)stream;
+  char* ws = (char*)workspace;
+  const int N = c.N, V = c.V, C = c.C, K = c.K;
+  const float inv_tau = 1.f / c.tau;
+  int* ids = K ? (int*)(ws + hp.ids) : nullptr;
+  float* share = K ? (float*)(ws + hp.share) : nullptr;
+  float* entropy = K && !c.bwd ? (float*)(ws + hp.entropy) : nullptr;
+  int* flags = K ? (int*)(ws + hp.flags) : nullptr;
+  int *row_of = (int*)(ws + hp.row_of), *pos = (int*)(ws + hp.pos),
+      *n_kept = (int*)(ws + hp.n_kept);
+  void* xc = ws + hp.xc;
+
+  if (K) {
+    const unsigned blocks = (unsigned)std::min<long>((N + kTeacherWarps - 1L) / kTeacherWarps, 148L * 16);
+    const size_t smem = (size_t)kTeacherWarps * K * 4;
+    if (c.t_dtype == ATTN_F32)
+      ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_teacher_kernel<float>, blocks, 32 * kTeacherWarps, smem, st,
+                                               c.t_idx, (const float*)c.t_logit, inv_tau, c.dloss, c.dlse,
+                                               ids, share, entropy, flags, N, V, K));
+    else
+      ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_teacher_kernel<__nv_bfloat16>, blocks, 32 * kTeacherWarps, smem, st,
+                                               c.t_idx, (const __nv_bfloat16*)c.t_logit, inv_tau, c.dloss, c.dlse,
+                                               ids, share, entropy, flags, N, V, K));
+  }
+  const int row_blocks = (int)std::min<long>((N + 7L) / 8, 296L);
+  const int rows_per_block = (N + row_blocks - 1) / row_blocks;
+  ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_rows_kernel, (unsigned)row_blocks, kRowThreads, 0, st,
+                                           K ? nullptr : c.target, flags, c.dloss, c.dlse,
+                                           (const uint4*)c.x, (uint4*)xc, row_of, pos, n_kept, N, V,
+                                           C / 8, rows_per_block));
+  if (launch_status()) return ATTN_ECUDA;
+
+  Maps maps = {};
+  Params p = {};
+  p.N = N;
+  p.V = V;
+  p.C = C;
+  p.K = std::max(K, 1);
+  p.inv_tau = inv_tau;
+  p.n_kept = n_kept;
+  p.row_of = row_of;
+  p.ids = K ? ids : c.target;
+  p.share = share;
+  p.row_pitch = hp.rows_pad;
+  if (!head_map(&maps.x_k, c.x, false, N, C, C, 128) ||
+      !head_map(&maps.xc_k, xc, false, hp.rows_pad, C, C, 128) ||
+      !head_map(&maps.w_k, c.w, false, V, C, C, 128))
+    return ATTN_ECUDA;
+
+  if (!c.bwd) {
+    p.part = (float2*)(ws + hp.part);
+    p.named = (float*)(ws + hp.named);
+    p.n_jobs = 1;
+    p.job[0] = {JOB_LSE, 0, V, 0, 0};
+    if (int rc = head_gemm(maps, p, st)) return rc;
+    ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_loss_kernel, (unsigned)((N + kLossRows - 1) / kLossRows),
+                                             kLossRows * kLossSlices, 0, st, p.part, p.named, share, entropy,
+                                             pos, c.loss, c.lse_out, N, p.K, hp.parts, hp.rows_pad));
+    return launch_status();
+  }
+
+  float* acc = (float*)(ws + hp.acc);
+  p.lse = c.lse;
+  p.dloss = c.dloss;
+  p.dlse = c.dlse;
+  p.kb_first = (std::min(hp.piece, V) + kKB - 1) / kKB;
+  p.dw_f32 = c.dw_dtype == ATTN_F32;
+  p.c_blocks = C % 64 == 0;
+  bool ok = head_map(&maps.dx_out, acc, true, hp.acc_rows, C, C, 32) &&
+            head_map(&maps.dw_out, c.dw, p.dw_f32 != 0, V, C, C, 32);
+  if (p.c_blocks)
+    ok = ok && head_block_map(&maps.x_mn, c.x, N, C) &&
+         head_block_map(&maps.xc_mn, xc, hp.rows_pad, C) && head_block_map(&maps.w_mn, c.w, V, C);
+  else
+    ok = ok && head_map(&maps.x_mn, c.x, false, N, C, C, kKB) &&
+         head_map(&maps.xc_mn, xc, false, hp.rows_pad, C, C, kKB) &&
+         head_map(&maps.w_mn, c.w, false, V, C, C, kKB);
+  for (int b = 0; b < std::min(hp.pieces, 2); ++b) {
+    const void* dz = ws + hp.dz[b];
+    ok = ok && head_map(&maps.dz_k[b], dz, false, hp.rows_pad, hp.piece, hp.piece, 128) &&
+         head_block_map(&maps.dz_mn[b], dz, hp.rows_pad, hp.piece) &&
+         head_map(&maps.dz_out[b], dz, false, hp.rows_pad, hp.piece, hp.piece, 32);
+  }
+  if (!ok) return ATTN_ECUDA;
+  auto job = [&](int kind, int piece) {
+    const int v0 = piece * hp.piece;
+    return Job{kind, v0, std::min(hp.piece, V - v0), piece & 1, piece > 0 ? 1 : 0};
+  };
+  // dz of piece 0; then dx and dW of a piece with dz of the next one (in the
+  // other buffer), the long units first
+  for (int i = -1; i < hp.pieces; ++i) {
+    p.n_jobs = 0;
+    if (i >= 0) {
+      p.job[p.n_jobs++] = job(JOB_DX, i);
+      p.job[p.n_jobs++] = job(JOB_DW, i);
+    }
+    if (i + 1 < hp.pieces) p.job[p.n_jobs++] = job(JOB_DZ, i + 1);
+    if (int rc = head_gemm(maps, p, st)) return rc;
+  }
+  const long n8 = (long)N * (C / 8);
+  ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_dx_kernel, (unsigned)std::min<long>((n8 + 255) / 256, 148L * 16),
+                                           256, 0, st, acc, pos, n_kept, (uint4*)c.dx, N, C,
+                                           p.kb_first));
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t attn_head_workspace_bytes(int N, int V, int C, int K, int is_bwd) {
+  if (!head_sizes_ok(N, V, C, K)) return 0;
+  return head_plan(N, V, C, K, is_bwd != 0).total;
+}
+
+int attn_head_ce(const void* x, const void* w, const int32_t* target, float* loss, float* lse,
+                 int N, int V, int C, void* workspace, size_t ws_bytes, void* stream) {
+  HeadCall c = {};
+  c.x = x;
+  c.w = w;
+  c.target = target;
+  c.tau = 1.f;
+  c.loss = loss;
+  c.lse_out = lse;
+  c.N = N;
+  c.V = V;
+  c.C = C;
+  return head_run(c, workspace, ws_bytes, stream);
+}
+
+int attn_head_ce_bwd(const void* x, const void* w, const int32_t* target, const float* lse,
+                     const float* dloss, const float* dlse, void* dx, void* dw, int N, int V,
+                     int C, int dw_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  HeadCall c = {};
+  c.x = x;
+  c.w = w;
+  c.target = target;
+  c.tau = 1.f;
+  c.lse = lse;
+  c.dloss = dloss;
+  c.dlse = dlse;
+  c.dx = dx;
+  c.dw = dw;
+  c.dw_dtype = dw_dtype;
+  c.N = N;
+  c.V = V;
+  c.C = C;
+  c.bwd = true;
+  return head_run(c, workspace, ws_bytes, stream);
+}
+
+int attn_head_distill(const void* x, const void* w, const int32_t* t_idx, const void* t_logit,
+                      float temperature, float* loss, float* lse, int N, int V, int C, int K,
+                      int t_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  if (K <= 0) return ATTN_EINVAL;
+  HeadCall c = {};
+  c.x = x;
+  c.w = w;
+  c.t_idx = t_idx;
+  c.t_logit = t_logit;
+  c.tau = temperature;
+  c.t_dtype = t_dtype;
+  c.loss = loss;
+  c.lse_out = lse;
+  c.N = N;
+  c.V = V;
+  c.C = C;
+  c.K = K;
+  return head_run(c, workspace, ws_bytes, stream);
+}
+
+int attn_head_distill_bwd(const void* x, const void* w, const int32_t* t_idx, const void* t_logit,
+                          float temperature, const float* lse, const float* dloss,
+                          const float* dlse, void* dx, void* dw, int N, int V, int C, int K,
+                          int t_dtype, int dw_dtype, void* workspace, size_t ws_bytes,
+                          void* stream) {
+  if (K <= 0) return ATTN_EINVAL;
+  HeadCall c = {};
+  c.x = x;
+  c.w = w;
+  c.t_idx = t_idx;
+  c.t_logit = t_logit;
+  c.tau = temperature;
+  c.t_dtype = t_dtype;
+  c.lse = lse;
+  c.dloss = dloss;
+  c.dlse = dlse;
+  c.dx = dx;
+  c.dw = dw;
+  c.dw_dtype = dw_dtype;
+  c.N = N;
+  c.V = V;
+  c.C = C;
+  c.K = K;
+  c.bwd = true;
+  return head_run(c, workspace, ws_bytes, stream);
+}
+
+}  // extern "C"

@@ -20,12 +20,14 @@ enum KernelKind : int {
   KK_GEMM,
   KK_ROPE_GRAD,
   KK_FILL,
+  KK_HEAD_GEMM,
+  KK_HEAD_ROWS,
   KK_COUNT
 };
 
 static const char* const kKernelNames[KK_COUNT] = {
     "doc_ranges", "rope_prep", "fwd", "delta", "dkdv", "dq", "dq_finalize", "decode",
-    "decode_combine", "gemm", "rope_grad", "fill"};
+    "decode_combine", "gemm", "rope_grad", "fill", "head_gemm", "head_rows"};
 
 namespace trace {
 

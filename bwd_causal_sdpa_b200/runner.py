@@ -256,3 +256,72 @@ class ProjRunner:
         f = lambda t: t.detach().to(torch.float64).cpu().numpy()
         return {n: f(getattr(self, n)) for n in
                 ("q", "k", "v", "y", "dx", "d_o", "dw_qkv", "dw_o")}
+
+
+class HeadRunner:
+    """Device buffers for the loss of the output head on one batch of rows (x,
+    W, the targets or the teacher's entries, loss, lse and the gradients) and
+    the attn_head_* calls on them."""
+
+    def __init__(self, w, device="cuda", stream: Optional[torch.cuda.Stream] = None,
+                 t_dtype: int = ATTN_F32, dw_dtype: int = ATTN_BF16, with_dlse: bool = True):
+        from . import attn_head_workspace_bytes
+
+        c = w.cfg
+        self.w = w
+        self.device = torch.device(device)
+        self.stream = stream
+        self.t_dtype, self.dw_dtype = t_dtype, dw_dtype
+        self.x = to_device(w.x, ATTN_BF16, self.device)
+        self.wt = to_device(w.w, ATTN_BF16, self.device)
+        i32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(self.device)
+        f32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(self.device)
+        self.target = self.t_idx = self.t_logit = None
+        if c.K:
+            self.t_idx = i32(w.t_idx)
+            self.t_logit = to_device(w.t_logit, t_dtype, self.device)
+        else:
+            self.target = i32(w.target)
+        self.dloss = f32(w.dloss)
+        self.dlse = f32(w.dlse) if with_dlse else None
+        self.loss = torch.empty(c.N, dtype=torch.float32, device=self.device)
+        self.lse = torch.empty_like(self.loss)
+        self.dx = torch.empty((c.N, c.C), dtype=torch.bfloat16, device=self.device)
+        self.dw = torch.empty((c.V, c.C), device=self.device,
+                              dtype=torch.float32 if dw_dtype == ATTN_F32 else torch.bfloat16)
+        self.ws_bytes = max(attn_head_workspace_bytes(c.N, c.V, c.C, c.K, b) for b in (0, 1))
+        self.ws = torch.empty(max(self.ws_bytes, 16), dtype=torch.uint8, device=self.device)
+
+    def forward(self) -> None:
+        from . import attn_head_ce, attn_head_distill
+
+        c = self.w.cfg
+        if c.K:
+            check(attn_head_distill(self.x, self.wt, self.t_idx, self.t_logit, c.tau, self.loss,
+                                    self.lse, c.N, c.V, c.C, c.K, self.t_dtype, self.ws,
+                                    self.ws_bytes, self.stream), "attn_head_distill")
+        else:
+            check(attn_head_ce(self.x, self.wt, self.target, self.loss, self.lse, c.N, c.V, c.C,
+                               self.ws, self.ws_bytes, self.stream), "attn_head_ce")
+
+    def backward(self) -> None:
+        from . import attn_head_ce_bwd, attn_head_distill_bwd
+
+        c = self.w.cfg
+        if c.K:
+            check(attn_head_distill_bwd(self.x, self.wt, self.t_idx, self.t_logit, c.tau, self.lse,
+                                        self.dloss, self.dlse, self.dx, self.dw, c.N, c.V, c.C,
+                                        c.K, self.t_dtype, self.dw_dtype, self.ws, self.ws_bytes,
+                                        self.stream), "attn_head_distill_bwd")
+        else:
+            check(attn_head_ce_bwd(self.x, self.wt, self.target, self.lse, self.dloss, self.dlse,
+                                   self.dx, self.dw, c.N, c.V, c.C, self.dw_dtype, self.ws,
+                                   self.ws_bytes, self.stream), "attn_head_ce_bwd")
+
+    def status(self) -> int:
+        return attn_get_status(self.stream)
+
+    def results(self) -> dict:
+        torch.cuda.synchronize(self.device)
+        f = lambda t: t.detach().to(torch.float64).cpu().numpy()
+        return {n: f(getattr(self, n)) for n in ("loss", "lse", "dx", "dw")}

@@ -333,6 +333,77 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
                       int B, int T, int C, int H, int D, void* stream);
 
 /*
+ * ---- Losses of the output head (logits never stored) ----
+ *
+ * The step after the last layer of a training decoder: logits z = x W^T / tau
+ * for N token rows against a vocabulary of V rows, and a loss per row that
+ * compares p = softmax over the vocabulary of z with a target distribution q
+ * of few entries (ARK README, the pipeline's cross-entropy through a stable
+ * log-sum-exp and its LM head; Forge README, "Architecture", the
+ * cross-entropy kernels). The logits are formed tile by tile on the tensor
+ * cores (bf16 operands, fp32 accumulation) and never written; lse, softmax
+ * statistics, losses and dx sums are fp32.
+ *
+ *   attn_head_ce:      q = 1 at target[n] (tau = 1):
+ *                      loss[n] = lse[n] - z[n][target[n]]
+ *   attn_head_distill: a teacher's K entries per row, q = softmax over them of
+ *                      t_logit / tau:
+ *                      loss[n] = sum_k q_k (log q_k - log p[n][id_k])
+ *   both:              lse[n] = log sum_v exp z[n][v]  (natural log)
+ *
+ * and, for upstream gradients dloss of loss and dlse of lse (dlse may be NULL;
+ * it carries, for example, the gradient of a penalty on lse^2):
+ *   dz[n][v] = ((dloss[n] + dlse[n]) p[n][v] - dloss[n] q[n][v]) / tau
+ *   dx = dz W, dw = dz^T x
+ *
+ * Layouts (row-major, contiguous, device pointers owned by the caller):
+ *   x, dx:   [N, C] bf16            w: [V, C] bf16
+ *   dw:      [V, C] in dw_dtype (ATTN_BF16 or ATTN_F32)
+ *   target:  [N] int32; a negative target leaves its row out
+ *   t_idx:   [N, K] int32 vocabulary ids, in any order; a negative id is an
+ *            absent entry; an id named twice counts twice
+ *   t_logit: [N, K] in t_dtype (ATTN_BF16 or ATTN_F32); what an absent entry
+ *            holds is not read into the result; -inf gives the entry q = 0
+ *   loss, lse, dloss, dlse: [N] float32
+ * A row without a target, or without an entry above -inf, is left out: its
+ * loss, lse and dx are 0, it adds nothing to dw, and what its x holds (NaN
+ * included) reaches nothing. The backward also leaves out a row whose dloss
+ * and dlse are both 0. The products cost what the rows that are kept cost;
+ * with none kept dx and dw are 0. A target or id >= V is treated as absent
+ * and the status word reports ATTN_EDEVICE_INPUT. Every output is overwritten.
+ *
+ * lse given to the backward is what the forward wrote for the same x, w and
+ * temperature. dz is rounded once to bf16, the tensor cores' operand type
+ * (2^-9 relative at most), before its two products: dw carries that rounding
+ * in either type. Results do not depend on atomics: the same call gives the
+ * same bits.
+ *
+ * Sizes: N, V, C >= 1, C a multiple of 8, K at most 1024; N and V at most
+ * 2^26, C at most 2^20 (else ATTN_EUNSUPPORTED). temperature is positive and
+ * finite. x, w, dx, dw and the workspace 16-byte aligned, the others to their
+ * element. Asynchronous on `stream`, like the attention calls.
+ *
+ * Workspace: attn_head_workspace_bytes(N, V, C, K, is_bwd) bytes, K = 0 for
+ * attn_head_ce*; 0 for invalid sizes. The backward takes the vocabulary in
+ * pieces, so its workspace does not grow with V: about 2 x 128 MiB for dz plus
+ * the fp32 sums of dx. Pure host function.
+ */
+size_t attn_head_workspace_bytes(int N, int V, int C, int K, int is_bwd);
+int attn_head_ce(const void* x, const void* w, const int32_t* target, float* loss, float* lse,
+                 int N, int V, int C, void* workspace, size_t ws_bytes, void* stream);
+int attn_head_ce_bwd(const void* x, const void* w, const int32_t* target, const float* lse,
+                     const float* dloss, const float* dlse, void* dx, void* dw, int N, int V,
+                     int C, int dw_dtype, void* workspace, size_t ws_bytes, void* stream);
+int attn_head_distill(const void* x, const void* w, const int32_t* t_idx, const void* t_logit,
+                      float temperature, float* loss, float* lse, int N, int V, int C, int K,
+                      int t_dtype, void* workspace, size_t ws_bytes, void* stream);
+int attn_head_distill_bwd(const void* x, const void* w, const int32_t* t_idx, const void* t_logit,
+                          float temperature, const float* lse, const float* dloss,
+                          const float* dlse, void* dx, void* dw, int N, int V, int C, int K,
+                          int t_dtype, int dw_dtype, void* workspace, size_t ws_bytes,
+                          void* stream);
+
+/*
  * Tracing aids (the source pages define no counterpart; they support
  * measurement only). Not thread safe: call them from the thread that
  * launches the attention calls.

@@ -19,10 +19,19 @@ the training forward, a closed form and invariants. No function here is
 and head layout, the output projection, and their backward products) is
 pinned against brute-force sums, finite differences and the attention
 oracle's own RoPE (rotating in the projection equals rotating in the
-attention).
+attention). ``oracle.head`` (the losses of the output head and their
+gradients) is pinned against float64 PyTorch's cross-entropy and KL divergence
+with their autograd, closed forms and central finite differences.
 """
 
 from .decode import decode_forward
+from .head import (
+    head_dz,
+    head_loss,
+    head_loss_backward,
+    target_lists,
+    teacher_lists,
+)
 from .projection import (
     out_projection,
     out_projection_backward,
@@ -42,6 +51,11 @@ from .attention import (
 
 __all__ = [
     "decode_forward",
+    "head_dz",
+    "head_loss",
+    "head_loss_backward",
+    "target_lists",
+    "teacher_lists",
     "out_projection",
     "out_projection_backward",
     "qkv_projection",

@@ -14,6 +14,13 @@ from .decode import (
     decode_config_by_name,
     make_decode_workload,
 )
+from .head import (
+    HEAD_CONFIGS,
+    HeadConfig,
+    HeadWorkload,
+    head_config_by_name,
+    make_head_workload,
+)
 from .projection import (
     PROJ_CONFIGS,
     ProjConfig,
@@ -36,6 +43,11 @@ __all__ = [
     "DecodeWorkload",
     "decode_config_by_name",
     "make_decode_workload",
+    "HEAD_CONFIGS",
+    "HeadConfig",
+    "HeadWorkload",
+    "head_config_by_name",
+    "make_head_workload",
     "PROJ_CONFIGS",
     "ProjConfig",
     "ProjWorkload",
