@@ -204,6 +204,8 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
 
   Maps maps = {};
   Params p = {};
+  p.x = (const uint4*)c.x;
+  p.w = (const uint4*)c.w;
   p.N = N;
   p.V = V;
   p.C = C;

@@ -47,7 +47,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kPairs = 74;            // CTA pairs of a full persistent grid (148 SMs)
 
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;  // TMA warp, MMA warp, epilogue warps
+constexpr int kThreads = 96 + 32 * kEpiWarps;  // TMA, MMA, epilogue warps, target warp
 constexpr int kSmRing = 0;
 constexpr int kSmStage = kStages * kStageBytes;          // 4 KB per epilogue warp
 constexpr int kSmBars = kSmStage + kEpiWarps * 4096;
@@ -78,6 +78,7 @@ struct Maps {
 };
 
 struct Params {
+  const uint4 *x, *w;
   int N, V, C;
   int K;                 // named ids per row (1: the target)
   int n_jobs;
@@ -204,6 +205,27 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y,
                : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// mma_ss_pair by the lanes with `issue` set, without a branch.
+__device__ __forceinline__ void mma_pair_if(uint32_t issue, uint32_t d_tmem, uint64_t a_desc,
+                                            uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+      : "memory");
+}
+
 // 128 rows (K contiguous: row0.., K from k0) or 128 columns (row index
 // contiguous: from row0, 64 K rows from k0) of an operand into dst.
 __device__ __forceinline__ void load_operand(const CUtensorMap* m, bool mn, bool one_box, int row0,
@@ -286,82 +308,131 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int u0 = (int)blockIdx.x >> 1, ustep = (int)gridDim.x >> 1;
 
+  // The TMA and MMA warps run their loops converged, one elected lane issuing:
+  // the operands of the issue then live in uniform registers. Issued from a
+  // branch of one thread, a tcgen05.mma cost 130 cycles whatever its size;
+  // so, 64 cycles at N = 128 and 128 at N = 256, the tensor core's own time.
   if (warp == 0) {
     // ---------------- TMA ----------------
-    if (lane == 0) {
-      const bool all = kept == p.N;  // every row kept: x is read in place
-      int it = 0;
-      bool ok = true;
-      Unit un;
-      for (int u = u0; ok && find_unit(u, p.n_jobs, dims, un); u += ustep) {
-        const Job& j = p.job[un.job];
-        const CUtensorMap *ma, *mb;
-        bool a_mn = false, b_mn = true, a_one = true, b_one = p.c_blocks != 0;
-        int ak = 0, bk = 0, brow = un.tn * kTile + rank * 128;
-        if (j.kind <= JOB_DZ) {
-          ma = all ? &maps.x_k : &maps.xc_k;
-          mb = &maps.w_k;
-          b_mn = false;
-          brow += j.v0;
-        } else if (j.kind == JOB_DX) {
-          ma = &maps.dz_k[j.buf];
-          mb = &maps.w_mn;
-          bk = j.v0;
-        } else {
-          ma = &maps.dz_mn[j.buf];
-          mb = all ? &maps.x_mn : &maps.xc_mn;
-          a_mn = true;
+    const bool el = elect_one();
+    const bool all = kept == p.N;  // every row kept: x is read in place
+    int s = 0;
+    uint32_t phase = 1;  // a fresh barrier's previous phase counts as complete
+    bool ok = true;
+    Unit un;
+    for (int u = u0; ok && find_unit(u, p.n_jobs, dims, un); u += ustep) {
+      const Job& j = p.job[un.job];
+      const CUtensorMap *ma, *mb;
+      bool a_mn = false, b_mn = true, b_one = p.c_blocks != 0;
+      int bk = 0, brow = un.tn * kTile + rank * 128;
+      if (j.kind <= JOB_DZ) {
+        ma = all ? &maps.x_k : &maps.xc_k;
+        mb = &maps.w_k;
+        b_mn = false;
+        brow += j.v0;
+      } else if (j.kind == JOB_DX) {
+        ma = &maps.dz_k[j.buf];
+        mb = &maps.w_mn;
+        bk = j.v0;
+      } else {
+        ma = &maps.dz_mn[j.buf];
+        mb = all ? &maps.x_mn : &maps.xc_mn;
+        a_mn = true;
+      }
+      const int arow = un.tm * kTile + rank * 128;
+      for (int kb = 0; kb < un.nkb; ++kb) {
+        if (!mbar_wait(bar(bEmpty + s), phase, abort_flag)) {
+          ok = false;
+          break;
         }
-        const int arow = un.tm * kTile + rank * 128;
-        for (int kb = 0; kb < un.nkb; ++kb, ++it) {
-          const int s = it % kStages, round = it / kStages;
-          if (it >= kStages && !mbar_wait(bar(bEmpty + s), (round - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
+        if (el) {
           // CTA 0's barrier counts the bytes of both CTAs' boxes
           if (rank == 0) mbar_arrive_expect_tx(bar(bFull + s), 2 * kStageBytes);
           const uint32_t full = map_rank(bar(bFull + s), 0);
           const uint32_t dst = sb0 + kSmRing + s * kStageBytes;
           const int k0 = (un.kb0 + kb) * kKB;
-          load_operand(ma, a_mn, a_one, arow, ak + k0, dst, full);
+          load_operand(ma, a_mn, true, arow, k0, dst, full);
           load_operand(mb, b_mn, b_one, brow, bk + k0, dst + kOperandBytes, full);
+        }
+        __syncwarp();
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1;
         }
       }
     }
   } else if (warp == 1) {
     // ---------------- MMA (CTA 0 issues for the pair) ----------------
-    if (lane == 0 && rank == 0) {
-      int it = 0, n = 0;
+    if (rank == 0) {
+      const uint32_t el = elect_one() ? 1u : 0u;
+      const uint64_t k_desc = smem_desc_sw128(sb0 + kSmRing, 16, 1024);
+      const uint64_t mn_desc = smem_desc_sw128(sb0 + kSmRing, 8192, 1024);
+      int s = 0, n = 0;
+      uint32_t phase = 0;
       bool ok = true;
       Unit un;
       for (int u = u0; ok && find_unit(u, p.n_jobs, dims, un); u += ustep, ++n) {
         const int kind = p.job[un.job].kind;
         const bool a_mn = kind == JOB_DW, b_mn = kind >= JOB_DX;
         const uint32_t idesc = idesc_f16(kTile, kTile, true, true, a_mn, b_mn);
+        // descriptors count in 16 bytes: 16 K values are 32 bytes along a row
+        // of K, or 16 rows of 128 bytes
+        const uint64_t a0 = a_mn ? mn_desc : k_desc;
+        const uint64_t b0 = (b_mn ? mn_desc : k_desc) + (kOperandBytes >> 4);
+        const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;
         const int a = n & 1;
         if (n >= 2 && !mbar_wait_cl(bar(bAccEmpty + a), ((n >> 1) - 1) & 1, abort_flag)) break;
         tc_fence_after();
         const uint32_t acc = tmem + a * kTile;
-        for (int kb = 0; kb < un.nkb; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!mbar_wait_cl(bar(bFull + s), (it / kStages) & 1, abort_flag)) {
+        uint32_t on = 0;
+        for (int kb = 0; kb < un.nkb; ++kb) {
+          if (!mbar_wait_cl(bar(bFull + s), phase, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = sb0 + kSmRing + s * kStageBytes, sb = sa + kOperandBytes;
+          const uint64_t da = a0 + (uint32_t)(s * (kStageBytes >> 4));
+          const uint64_t db = b0 + (uint32_t)(s * (kStageBytes >> 4));
 #pragma unroll
           for (int kk = 0; kk < kKB / 16; ++kk) {
-            const uint64_t da = a_mn ? smem_desc_sw128(sa + kk * 2048, 8192, 1024)
-                                     : smem_desc_sw128(sa + kk * 32, 16, 1024);
-            const uint64_t db = b_mn ? smem_desc_sw128(sb + kk * 2048, 8192, 1024)
-                                     : smem_desc_sw128(sb + kk * 32, 16, 1024);
-            mma_ss_pair(acc, da, db, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+            mma_pair_if(el, acc, da + kk * a_step, db + kk * b_step, idesc, on);
+            on = 1;
           }
-          commit_pair(bar(bEmpty + s));
+          if (el) commit_pair(bar(bEmpty + s));
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
-        if (ok) commit_pair(bar(bAccFull + a));
+        if (ok && el) commit_pair(bar(bAccFull + a));
+        __syncwarp();
+      }
+    }
+  } else if (warp == 2 + kEpiWarps) {
+    // ---------------- the target's logit ----------------
+    // A single named id per row is a dot product of its own, in plain fp32: the
+    // loss is the difference lse - z, and the tensor core's sums, cut instead
+    // of rounded, would leave about 1e-6 of it. Runs beside the products.
+    if (p.n_jobs == 1 && p.job[0].kind == JOB_LSE && !p.share) {
+      const int c8 = p.C / 8;
+      for (int m = blockIdx.x; m < kept; m += gridDim.x) {
+        const int row = p.row_of[m];
+        const uint4* xr = p.x + (size_t)row * c8;
+        const uint4* wr = p.w + (size_t)p.ids[row] * c8;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
+        for (int i = lane; i < c8; i += 32) {
+          const uint4 a = xr[i], b = wr[i];
+          const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s0 = fmaf(__uint_as_float(av[e] << 16), __uint_as_float(bv[e] << 16), s0);
+            s1 = fmaf(__uint_as_float(av[e] & 0xffff0000u), __uint_as_float(bv[e] & 0xffff0000u), s1);
+          }
+        }
+        s0 = warp_sum(s0 + s1);
+        if (lane == 0) p.named[m] = s0 * p.inv_tau;
       }
     }
   } else {
@@ -388,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* share = nullptr;
       if (j.kind <= JOB_DZ && m < kept) {
         const int row = p.row_of[m];
-        nm.start(p.ids + (size_t)row * p.K, p.K, j.v0 + col0);
+        // the forward's single target has a warp of its own
+        if (j.kind == JOB_DZ || p.share) nm.start(p.ids + (size_t)row * p.K, p.K, j.v0 + col0);
         if (j.kind == JOB_DZ) {
           lse2 = p.lse[row] * kLog2e;
           const float g = p.dloss[row];
