@@ -9,18 +9,19 @@
 
 namespace {
 
-// Vocabulary rows per piece of the backward: the dz buffer of a piece (two
-// are in use) takes up to 128 MiB, or 4096 columns when the rows are many
+// Vocabulary rows per piece of the backward: the dz buffer of a piece (three
+// are in use) takes up to 96 MiB, or 2048 columns when the rows are many
 // (shorter pieces would add into dx more often than their products are worth).
-constexpr size_t kDzBytes = (size_t)128 << 20;
-constexpr long kDzMinCols = 4096;
+constexpr size_t kDzBytes = (size_t)96 << 20;
+constexpr long kDzMinCols = 2048;
 
 struct HeadPlan {
   int rows_pad = 0, piece = 0, pieces = 0, parts = 0;
-  size_t n_kept = 0, row_of = 0, pos = 0, xc = 0, ids = 0, share = 0, entropy = 0, flags = 0;
+  size_t n_kept = 0, ctl = 0, row_of = 0, pos = 0, par = 0, xc = 0, ids = 0, share = 0, entropy = 0, flags = 0;
   size_t part = 0, named = 0;     // forward
-  size_t dz[2] = {0, 0}, acc = 0; // backward
+  size_t dz[head100::kDzBuffers] = {}, acc = 0;  // backward
   long acc_rows = 0;
+  int n_ctl = 0;
   size_t total = 0;
 };
 
@@ -44,7 +45,17 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
     return at;
   };
   p.rows_pad = (N + kTile - 1) / kTile * kTile;
+  long cols = ((long)V + kTile - 1) / kTile * kTile;
+  if (bwd)
+    cols = std::min(cols, std::max((long)(kDzBytes / ((size_t)p.rows_pad * 2)) / kTile * kTile,
+                                   kDzMinCols));
+  p.pieces = (int)((V + cols - 1) / cols);
+  p.piece = (int)(((V + p.pieces - 1) / p.pieces + kTile - 1) / kTile * kTile);
+  p.pieces = (V + p.piece - 1) / p.piece;
+  p.n_ctl = kCtlPieces + 3 * p.pieces + kPairs * 2 * kEpiWarps;
   p.n_kept = take(4);
+  p.ctl = take((size_t)p.n_ctl * 4);
+  p.par = take((size_t)p.rows_pad * sizeof(RowPar));
   p.row_of = take((size_t)p.rows_pad * 4);
   p.pos = take((size_t)N * 4);
   p.xc = take((size_t)p.rows_pad * C * 2);
@@ -61,13 +72,7 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
     p.total = off;
     return p;
   }
-  const long v_pad = ((long)V + kTile - 1) / kTile * kTile;
-  long cols = (long)(kDzBytes / ((size_t)p.rows_pad * 2)) / kTile * kTile;
-  cols = std::min(v_pad, std::max(cols, kDzMinCols));
-  p.pieces = (int)((V + cols - 1) / cols);
-  p.piece = (int)(((V + p.pieces - 1) / p.pieces + kTile - 1) / kTile * kTile);
-  p.pieces = (V + p.piece - 1) / p.piece;
-  for (int b = 0; b < std::min(p.pieces, 2); ++b)
+  for (int b = 0; b < std::min(p.pieces, kDzBuffers); ++b)
     p.dz[b] = take((size_t)p.rows_pad * p.piece * 2);
   // the accumulators of dx: the most rows that any number of kept rows takes
   const int tn = (C + kTile - 1) / kTile, kb = (std::min(p.piece, V) + kKB - 1) / kKB;
@@ -151,17 +156,16 @@ int head_check(const HeadCall& c, void* ws, size_t ws_bytes) {
   return ATTN_OK;
 }
 
+template <bool kBwd>
 int head_gemm(const head100::Maps& maps, const head100::Params& p, cudaStream_t st) {
   using namespace head100;
   static bool smem_done[64];
-  if (!ensure_smem(head_gemm_kernel, kSmAlloc, smem_done)) return ATTN_ECUDA;
-  long units = 0;
-  for (int j = 0; j < p.n_jobs; ++j) units += job_dims(p.job[j], p.N, p.C, p.kb_first).units;
-  // fewer kept rows may mean more parts of dx, never more than two per pair
-  for (int j = 0; j < p.n_jobs; ++j)
-    if (p.job[j].kind == JOB_DX) units = std::max<long>(units, kPairs);
+  if (!ensure_smem(head_gemm_kernel<kBwd>, kSmAlloc, smem_done)) return ATTN_ECUDA;
+  // pairs beyond the units that any number of kept rows gives would be idle
+  const Sched s = make_sched(p, p.N);
+  const long units = kBwd ? kPairs : s.dz(0);
   const unsigned pairs = (unsigned)std::min<long>(units, kPairs);
-  ATTN_LAUNCH(KK_HEAD_GEMM, st, pdl_cluster_launch(head_gemm_kernel, dim3(2 * pairs), kThreads,
+  ATTN_LAUNCH(KK_HEAD_GEMM, st, pdl_cluster_launch(head_gemm_kernel<kBwd>, dim3(2 * pairs), kThreads,
                                                    kSmAlloc, st, 2u, maps, p));
   return launch_status();
 }
@@ -194,12 +198,28 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
                                                c.t_idx, (const __nv_bfloat16*)c.t_logit, inv_tau, c.dloss, c.dlse,
                                                ids, share, entropy, flags, N, V, K));
   }
-  const int row_blocks = (int)std::min<long>((N + 7L) / 8, 296L);
-  const int rows_per_block = (N + row_blocks - 1) / row_blocks;
-  ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_rows_kernel, (unsigned)row_blocks, kRowThreads, 0, st,
-                                           K ? nullptr : c.target, flags, c.dloss, c.dlse,
-                                           (const uint4*)c.x, (uint4*)xc, row_of, pos, n_kept, N, V,
-                                           C / 8, rows_per_block));
+  RowsArgs ra = {};
+  ra.target = K ? nullptr : c.target;
+  ra.flags = flags;
+  ra.lse = c.lse;
+  ra.dloss = c.dloss;
+  ra.dlse = c.dlse;
+  ra.x = (const uint4*)c.x;
+  ra.xc = (uint4*)xc;
+  ra.dx = (uint4*)c.dx;
+  ra.row_of = row_of;
+  ra.pos = pos;
+  ra.n_kept = n_kept;
+  ra.par = (RowPar*)(ws + hp.par);
+  ra.ctl = (unsigned*)(ws + hp.ctl);
+  ra.n_ctl = hp.n_ctl;
+  ra.N = N;
+  ra.V = V;
+  ra.c8 = C / 8;
+  ra.inv_tau = inv_tau;
+  const int row_blocks = (int)std::min<long>((N + 15L) / 16, 148L);
+  ra.rows_per_block = (N + row_blocks - 1) / row_blocks;
+  ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_rows_kernel, (unsigned)row_blocks, kRowThreads, 0, st, ra));
   if (launch_status()) return ATTN_ECUDA;
 
   Maps maps = {};
@@ -213,6 +233,10 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   p.inv_tau = inv_tau;
   p.n_kept = n_kept;
   p.row_of = row_of;
+  p.par = ra.par;
+  p.ctl = ra.ctl;
+  p.piece = hp.piece;
+  p.pieces = hp.pieces;
   p.ids = K ? ids : c.target;
   p.share = share;
   p.row_pitch = hp.rows_pad;
@@ -224,23 +248,18 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   if (!c.bwd) {
     p.part = (float2*)(ws + hp.part);
     p.named = (float*)(ws + hp.named);
-    p.n_jobs = 1;
-    p.job[0] = {JOB_LSE, 0, V, 0, 0};
-    if (int rc = head_gemm(maps, p, st)) return rc;
+    if (int rc = head_gemm<false>(maps, p, st)) return rc;
     ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_loss_kernel, (unsigned)((N + kLossRows - 1) / kLossRows),
                                              kLossRows * kLossSlices, 0, st, p.part, p.named, share, entropy,
                                              pos, c.loss, c.lse_out, N, p.K, hp.parts, hp.rows_pad));
     return launch_status();
   }
 
-  float* acc = (float*)(ws + hp.acc);
-  p.lse = c.lse;
-  p.dloss = c.dloss;
-  p.dlse = c.dlse;
-  p.kb_first = (std::min(hp.piece, V) + kKB - 1) / kKB;
+  p.acc = (const float*)(ws + hp.acc);
+  p.dx = (__nv_bfloat16*)c.dx;
   p.dw_f32 = c.dw_dtype == ATTN_F32;
   p.c_blocks = C % 64 == 0;
-  bool ok = head_map(&maps.dx_out, acc, true, hp.acc_rows, C, C, 32) &&
+  bool ok = head_map(&maps.dx_out, p.acc, true, hp.acc_rows, C, C, 32) &&
             head_map(&maps.dw_out, c.dw, p.dw_f32 != 0, V, C, C, 32);
   if (p.c_blocks)
     ok = ok && head_block_map(&maps.x_mn, c.x, N, C) &&
@@ -249,33 +268,14 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
     ok = ok && head_map(&maps.x_mn, c.x, false, N, C, C, kKB) &&
          head_map(&maps.xc_mn, xc, false, hp.rows_pad, C, C, kKB) &&
          head_map(&maps.w_mn, c.w, false, V, C, C, kKB);
-  for (int b = 0; b < std::min(hp.pieces, 2); ++b) {
+  for (int b = 0; b < std::min(hp.pieces, kDzBuffers); ++b) {
     const void* dz = ws + hp.dz[b];
     ok = ok && head_map(&maps.dz_k[b], dz, false, hp.rows_pad, hp.piece, hp.piece, 128) &&
          head_block_map(&maps.dz_mn[b], dz, hp.rows_pad, hp.piece) &&
          head_map(&maps.dz_out[b], dz, false, hp.rows_pad, hp.piece, hp.piece, 32);
   }
   if (!ok) return ATTN_ECUDA;
-  auto job = [&](int kind, int piece) {
-    const int v0 = piece * hp.piece;
-    return Job{kind, v0, std::min(hp.piece, V - v0), piece & 1, piece > 0 ? 1 : 0};
-  };
-  // dz of piece 0; then dx and dW of a piece with dz of the next one (in the
-  // other buffer), the long units first
-  for (int i = -1; i < hp.pieces; ++i) {
-    p.n_jobs = 0;
-    if (i >= 0) {
-      p.job[p.n_jobs++] = job(JOB_DX, i);
-      p.job[p.n_jobs++] = job(JOB_DW, i);
-    }
-    if (i + 1 < hp.pieces) p.job[p.n_jobs++] = job(JOB_DZ, i + 1);
-    if (int rc = head_gemm(maps, p, st)) return rc;
-  }
-  const long n8 = (long)N * (C / 8);
-  ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_dx_kernel, (unsigned)std::min<long>((n8 + 255) / 256, 148L * 16),
-                                           256, 0, st, acc, pos, n_kept, (uint4*)c.dx, N, C,
-                                           p.kb_first));
-  return launch_status();
+  return head_gemm<true>(maps, p, st);
 }
 
 }  // namespace

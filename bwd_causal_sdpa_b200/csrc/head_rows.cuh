@@ -9,7 +9,6 @@
 
 namespace head100 {
 
-constexpr int kRowThreads = 256;
 constexpr int kTeacherWarps = 4;
 constexpr int kMaxNamed = 1024;  // teacher entries per row
 
@@ -19,30 +18,49 @@ __device__ __forceinline__ bool has_weight(const float* dloss, const float* dlse
 }
 
 // Compacts the kept rows: row_of (kept row -> row), pos (row -> kept row or
-// -1), their number, and, unless all are kept, their x rows in xc, followed by
-// zero rows up to a multiple of the tile (K values of dz^T x). Order is kept.
-// Every block counts the rows before its own from the flags themselves (4
-// bytes per row, read from L2), so there is one launch and no pass between.
+// -1), their number, what each brings to the epilogues (par), and, unless all
+// are kept, their x rows in xc, followed by zero rows up to a multiple of the
+// tile (K values of dz^T x). Order is kept. Every block counts the rows before
+// its own from the flags themselves (read from L2, several at a time), so
+// there is one launch and no pass between. Also clears ctl, and dx of the rows
+// left out.
 // flags: [N] non-zero where the row counts; or null: target in [0, V) and an
 // upstream gradient that is not zero. A target >= V is reported.
-__global__ void __launch_bounds__(kRowThreads)
-    head_rows_kernel(const int* __restrict__ target, const int* __restrict__ flags,
-                     const float* __restrict__ dloss, const float* __restrict__ dlse,
-                     const uint4* __restrict__ x, uint4* __restrict__ xc, int* __restrict__ row_of,
-                     int* __restrict__ pos, int* __restrict__ n_kept, int N, int V, int c8,
-                     int rows_per_block) {
+struct RowsArgs {
+  const int *target, *flags;
+  const float *lse, *dloss, *dlse;  // null in the forward (dlse: or when absent)
+  const uint4* x;
+  uint4 *xc, *dx;  // dx: null in the forward
+  int *row_of, *pos, *n_kept;
+  RowPar* par;
+  unsigned* ctl;
+  int n_ctl;
+  int N, V, c8, rows_per_block;
+  float inv_tau;
+};
+constexpr int kRowThreads = 512;
+__global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowsArgs a) {
   pdl_wait_and_trigger();
-  __shared__ int s_sum[2][kRowThreads / 32];
-  __shared__ int s_warp[kRowThreads / 32];
+  constexpr int kWarps = kRowThreads / 32;
+  __shared__ int s_sum[2][kWarps];
+  __shared__ int s_warp[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r0 = blockIdx.x * rows_per_block, r1 = min(N, r0 + rows_per_block);
-  auto counts = [&](int r) -> bool {
-    if (flags) return flags[r] != 0;
-    return (unsigned)target[r] < (unsigned)V && has_weight(dloss, dlse, r);
+  const int r0 = blockIdx.x * a.rows_per_block, r1 = min(a.N, r0 + a.rows_per_block);
+  for (int i = blockIdx.x * kRowThreads + tid; i < a.n_ctl; i += gridDim.x * kRowThreads)
+    a.ctl[i] = 0;
+  auto counts = [&](int r) -> int {
+    if (a.flags) return a.flags[r] != 0;
+    int k = (unsigned)a.target[r] < (unsigned)a.V;
+    if (a.dloss) {
+      const float g = a.dloss[r], h = a.dlse ? a.dlse[r] : 0.f;
+      k &= (g != 0.f) | (h != 0.f);
+    }
+    return k;
   };
   int before = 0, total = 0;
-  for (int r = tid; r < N; r += kRowThreads) {
-    const int k = counts(r) ? 1 : 0;
+#pragma unroll 8
+  for (int r = tid; r < a.N; r += kRowThreads) {
+    const int k = counts(r);
     total += k;
     before += r < r0 ? k : 0;
   }
@@ -56,41 +74,53 @@ __global__ void __launch_bounds__(kRowThreads)
   }
   __syncthreads();
   before = total = 0;
-  for (int w = 0; w < kRowThreads / 32; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     before += s_sum[0][w];
     total += s_sum[1][w];
   }
-  if (blockIdx.x == 0 && tid == 0) *n_kept = total;
+  if (blockIdx.x == 0 && tid == 0) *a.n_kept = total;
   for (int b = r0; b < r1; b += kRowThreads) {
     const int r = b + tid;
     const bool in = r < r1;
     const bool k = in && counts(r);
-    if (in && target && target[r] >= V) report_status(ATTN_EDEVICE_INPUT);
+    if (in && a.target && a.target[r] >= a.V) report_status(ATTN_EDEVICE_INPUT);
     const unsigned votes = __ballot_sync(0xffffffffu, k);
     if (lane == 0) s_warp[warp] = __popc(votes);
     __syncthreads();
     int at = before, all = 0;
-    for (int w = 0; w < kRowThreads / 32; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       at += w < warp ? s_warp[w] : 0;
       all += s_warp[w];
     }
     at += __popc(votes & ((1u << lane) - 1u));
-    if (in) pos[r] = k ? at : -1;
-    if (k) row_of[at] = r;
+    if (in) a.pos[r] = k ? at : -1;
+    if (k) {
+      a.row_of[at] = r;
+      RowPar rp = {0.f, 0.f, 0.f, a.target ? a.target[r] : r};
+      if (a.dloss) {
+        const float g = a.dloss[r];
+        rp.lse2 = a.lse[r] * kLog2e;
+        rp.ca = (g + (a.dlse ? a.dlse[r] : 0.f)) * a.inv_tau;
+        rp.cb = g * a.inv_tau;
+      }
+      a.par[at] = rp;
+    }
     before += all;
     __syncthreads();
   }
-  if (total == N) return;  // the products read x in place
+  if (total == a.N) return;  // the products read x in place
   // a warp copies a row at a time (its pos entries were written by this block)
-  for (int r = r0 + warp; r < r1; r += kRowThreads / 32) {
-    const int at = pos[r];
-    if (at < 0) continue;
-    for (int i = lane; i < c8; i += 32) xc[(size_t)at * c8 + i] = x[(size_t)r * c8 + i];
+  for (int r = r0 + warp; r < r1; r += kWarps) {
+    const int at = a.pos[r];
+    if (at >= 0) {
+      for (int i = lane; i < a.c8; i += 32) a.xc[(size_t)at * a.c8 + i] = a.x[(size_t)r * a.c8 + i];
+    } else if (a.dx) {
+      for (int i = lane; i < a.c8; i += 32) a.dx[(size_t)r * a.c8 + i] = make_uint4(0, 0, 0, 0);
+    }
   }
   const int pad = slot_rows(total);
-  for (int r = total + blockIdx.x * (kRowThreads / 32) + warp; r < pad;
-       r += gridDim.x * (kRowThreads / 32))
-    for (int i = lane; i < c8; i += 32) xc[(size_t)r * c8 + i] = make_uint4(0, 0, 0, 0);
+  for (int r = total + blockIdx.x * kWarps + warp; r < pad; r += gridDim.x * kWarps)
+    for (int i = lane; i < a.c8; i += 32) a.xc[(size_t)r * a.c8 + i] = make_uint4(0, 0, 0, 0);
 }
 
 // The teacher's list of one row per warp: q = softmax of t / tau over the
@@ -164,9 +194,9 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
 }
 
 // lse and loss of every row from the parts of its logits: 32 rows per block,
-// eight threads per row. loss = sum_k q_k (log q_k + lse - z_k), for a single
+// sixteen threads per row. loss = sum_k q_k (log q_k + lse - z_k), for a single
 // target lse - z.
-constexpr int kLossRows = 32, kLossSlices = 8;
+constexpr int kLossRows = 32, kLossSlices = 16;
 __global__ void __launch_bounds__(kLossRows* kLossSlices)
     head_loss_kernel(const float2* __restrict__ part, const float* __restrict__ named,
                      const float* __restrict__ share, const float* __restrict__ entropy,
@@ -183,20 +213,32 @@ __global__ void __launch_bounds__(kLossRows* kLossSlices)
     s = nm > -INFINITY ? s * exp2f(m - nm) + os * exp2f(om - nm) : s + os;
     m = nm;
   };
-  if (at >= 0)
-    for (int j = ty; j < parts; j += kLossSlices) {
-      const float2 t = part[(size_t)j * row_pitch + at];
-      join(t.x, t.y);
+  if (at >= 0) {
+    const float2* mine = part + at;
+    for (int j = ty; j < parts; j += 8 * kLossSlices) {
+      float2 t[8];  // eight loads in flight
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int q = j + i * kLossSlices;
+        t[i] = q < parts ? mine[(size_t)q * row_pitch] : make_float2(-INFINITY, 0.f);
+      }
+      float top = t[0].x;
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, t[i].x);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        sum += top > -INFINITY ? t[i].y * exp2f(t[i].x - top) : t[i].y;
+      join(top, sum);
     }
+  }
   s_m[ty][tx] = m;
   s_s[ty][tx] = s;
   __syncthreads();
-  for (int j = 0; j < kLossSlices; ++j)
-    if (j != ty) join(s_m[j][tx], s_s[j][tx]);
-  // every slice now has the row's total (equal up to the order of the sum);
-  // slice 0's is the row's lse
-  __syncthreads();
-  if (ty == 0) s_m[0][tx] = (m + log2f(s)) * kLn2;
+  if (ty == 0) {
+    for (int j = 1; j < kLossSlices; ++j) join(s_m[j][tx], s_s[j][tx]);
+    s_m[0][tx] = (m + log2f(s)) * kLn2;
+  }
   __syncthreads();
   const float l = s_m[0][tx];
   float d = 0.f;
@@ -212,37 +254,6 @@ __global__ void __launch_bounds__(kLossRows* kLossSlices)
     for (int j = 0; j < kLossSlices; ++j) d += s_s[j][tx];
     lse[r] = at >= 0 ? l : 0.f;
     loss[r] = at >= 0 ? (share ? entropy[r] + d : d) : 0.f;
-  }
-}
-
-// dx of every row: its accumulators added in order and rounded once; zeros
-// for a row that was left out. Eight columns per thread.
-__global__ void __launch_bounds__(256)
-    head_dx_kernel(const float* __restrict__ acc, const int* __restrict__ pos,
-                   const int* __restrict__ n_kept, uint4* __restrict__ dx, int N, int C,
-                   int kb_total) {
-  pdl_wait_and_trigger();
-  const int kept = *n_kept;
-  int splits, kb_per;
-  split_dx(((kept + kTile - 1) / kTile) * ((C + kTile - 1) / kTile), kb_total, splits, kb_per);
-  const size_t slot = (size_t)slot_rows(kept) * C;
-  const int c8 = C / 8;
-  const long n = (long)N * c8;
-  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256) {
-    const int r = (int)(i / c8), c = (int)(i - (long)r * c8) * 8;
-    const int at = pos[r];
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (at >= 0) {
-      const float* src = acc + (size_t)at * C + c;
-      for (int s = 0; s < splits; ++s, src += slot) {
-        const float4 a = *reinterpret_cast<const float4*>(src);
-        const float4 b = *reinterpret_cast<const float4*>(src + 4);
-        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
-      }
-    }
-    dx[i] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                       pack_bf16(v[6], v[7]));
   }
 }
 

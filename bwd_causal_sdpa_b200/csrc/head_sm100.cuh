@@ -22,10 +22,15 @@
 // kept rows cost, and what a left-out row holds (NaN included) reaches
 // nothing. Their number lives on the device; every kernel reads it there.
 //
-// One kernel runs all products, head_gemm_kernel: clusters of two CTAs, each
-// pair walking a strided list of 256 x 256 output tiles (units) of up to
-// three products that do not depend on one another; one launch of the
-// backward runs dx and dW of a piece and the logits of the next one.
+// One kernel, head_gemm_kernel, runs all products of a call in one launch:
+// clusters of two CTAs, each pair taking 256 x 256 output tiles (units) one
+// after the other from a common counter. The backward's units are ordered
+//     dz(0) dz(1) | dW(0) dx(0) dz(2) | dW(1) dx(1) dz(3) | ...
+// with dz in three buffers, so what a unit waits for (its piece's dz, the
+// readers of the buffer it overwrites, the previous piece's sums in dx) was
+// handed out a whole group of units earlier. Waits are on counters in global
+// memory and point only to units handed out before, so they end whatever the
+// number of CTAs that run at a time.
 #pragma once
 
 #include <limits.h>
@@ -39,7 +44,7 @@ using namespace sm100;
 
 constexpr int kTile = 256;            // output tile of a CTA pair (rows and columns)
 constexpr int kKB = 64;               // K values per ring stage
-constexpr int kStages = 6;
+constexpr int kStages = 5;  // 6 measured no faster; the room goes to the staging
 constexpr int kOperandBytes = 128 * kKB * 2;  // 128 rows (or columns) of a stage
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -47,67 +52,67 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kPairs = 74;            // CTA pairs of a full persistent grid (148 SMs)
 
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 96 + 32 * kEpiWarps;  // TMA, MMA, epilogue warps, target warp
+constexpr int kThreads = 96 + 32 * kEpiWarps;  // TMA, MMA, epilogue, hand-out / target warps
+constexpr int kDzBuffers = 3;
+constexpr int kTickets = 4;  // units known ahead, a ring in shared memory
 constexpr int kSmRing = 0;
-constexpr int kSmStage = kStages * kStageBytes;          // 4 KB per epilogue warp
-constexpr int kSmBars = kSmStage + kEpiWarps * 4096;
-constexpr int bFull = 0, bEmpty = kStages, bAccFull = 2 * kStages, bAccEmpty = 2 * kStages + 2;
-constexpr int kNumBars = 2 * kStages + 4;
-constexpr int kSmMisc = kSmBars + kNumBars * 8;
-constexpr int kSmJobs = kSmMisc + 16;
-constexpr int kSmAlloc = kSmJobs + 256;
+constexpr int kSmStage = kStages * kStageBytes;          // 2 x 4 KB per epilogue warp
+constexpr int kSmBars = kSmStage + kEpiWarps * 8192;
+constexpr int bFull = 0, bEmpty = kStages, bAccFull = 2 * kStages, bAccEmpty = 2 * kStages + 2,
+              bTkFull = 2 * kStages + 4, bTkEmpty = bTkFull + kTickets;
+constexpr int kNumBars = bTkEmpty + kTickets;
+constexpr int kSmTickets = kSmBars + kNumBars * 8;       // kTickets x 32 bytes
+constexpr int kSmMisc = kSmTickets + kTickets * 32;
+constexpr int kSmAlloc = kSmMisc + 16;
 static_assert(kSmAlloc <= 232448, "shared memory of one CTA");
+static_assert(kSmTickets % 16 == 0 && kSmStage % 1024 == 0, "alignment");
 
-enum Kind : int { JOB_LSE = 0, JOB_DZ = 1, JOB_DX = 2, JOB_DW = 3 };
-
-// One product. Vocabulary rows [v0, v0 + vn), dz in buffer `buf`.
-struct Job {
-  int kind, v0, vn, buf;
-  int add;  // JOB_DX: add to the accumulator (else store)
-};
-
-constexpr int kMaxJobs = 3;
+enum Kind : int { LSE = 0, DZ = 1, DX = 2, DW = 3, END = 4 };
 
 struct Maps {
   // operand loads: _k with K contiguous (boxes of 64 K x 128 rows), _mn with
   // the row index contiguous (boxes of 64 rows x 64 K, two of them in one box
   // when the extent is a multiple of 64)
-  CUtensorMap x_k, xc_k, w_k, x_mn, xc_mn, w_mn, dz_k[2], dz_mn[2];
+  CUtensorMap x_k, xc_k, w_k, x_mn, xc_mn, w_mn, dz_k[kDzBuffers], dz_mn[kDzBuffers];
   // output boxes of 32 rows x 128 bytes
-  CUtensorMap dz_out[2], dx_out, dw_out;
+  CUtensorMap dz_out[kDzBuffers], dx_out, dw_out;
+};
+
+// What a kept row brings to its logits' epilogue, by kept row: lse in base 2,
+// the factors of p and of q in dz, and its target (one named id) or its row.
+struct __align__(16) RowPar {
+  float lse2, ca, cb;
+  int id;
 };
 
 struct Params {
   const uint4 *x, *w;
   int N, V, C;
   int K;                 // named ids per row (1: the target)
-  int n_jobs;
-  Job job[kMaxJobs];
-  int kb_first;          // K blocks of dx over a whole piece
+  int piece, pieces;     // vocabulary rows per piece (all of V in the forward)
   int c_blocks;          // C % 64 == 0: _mn maps of x and W take both 64-wide blocks in one box
   int dw_f32;
   float inv_tau;
   const int* n_kept;     // rows kept (device)
   const int* row_of;     // kept row -> row
+  const RowPar* par;     // by kept row
   const int* ids;        // [N][K] ascending; a negative or >= V id matches nothing
   const float* share;    // [N][K] q, or null (1 at the target)
-  const float* lse;      // [N] (JOB_DZ)
-  const float* dloss;    // [N]
-  const float* dlse;     // [N] or null
-  float2* part;          // JOB_LSE: [2 tiles_n][row_pitch] maximum (base 2), sum
-  float* named;          // JOB_LSE: [kept row][K] z at the row's ids
+  float2* part;          // LSE: [2 tiles][row_pitch] maximum (base 2), sum
+  float* named;          // LSE: [kept row][K] z at the row's ids
   int row_pitch;
+  const float* acc;      // fp32 sums of dx, slot_rows(kept) rows per split
+  __nv_bfloat16* dx;
+  // zero at launch: [0] the next unit; then per piece finished dz, consumed dz,
+  // finished dx; then finished splits per warp region of the last piece's dx
+  unsigned* ctl;
 };
-
-// Tiles and K blocks of a job for `kept` rows.
-struct Dims {
-  int tiles_m, tiles_n, splits, kb_total, kb_per, units;
-};
+constexpr int kCtlPieces = 4;  // first per-piece counter in ctl, three per piece
 
 // dx has few tiles when few rows are kept: its K axis (the vocabulary) is
-// then split over units, each with an accumulator of its own that the closing
-// pass adds in order (no atomics, so results repeat). Two units per CTA pair,
-// at least eight K blocks each.
+// then split over units, each with an accumulator of its own that the last one
+// to finish adds in order (whoever that is: results repeat). Two units per CTA
+// pair, at least eight K blocks each.
 __host__ __device__ inline void split_dx(int tiles, int kb_total, int& splits, int& kb_per) {
   splits = 1;
   if (tiles > 0 && tiles < kPairs) {
@@ -121,69 +126,114 @@ __host__ __device__ inline void split_dx(int tiles, int kb_total, int& splits, i
   if (splits < 1) splits = 1;
 }
 
-// kb_first: K blocks of a whole piece. A shorter last piece keeps the parts'
-// length, so it adds into accumulators that the first piece has written.
-__host__ __device__ inline Dims job_dims(const Job& j, int kept, int C, int kb_first) {
-  Dims d;
-  const int rows = (kept + kTile - 1) / kTile, cols = (C + kTile - 1) / kTile,
-            voc = (j.vn + kTile - 1) / kTile;
-  d.splits = 1;
-  if (j.kind == JOB_LSE || j.kind == JOB_DZ) {
-    d.tiles_m = rows;
-    d.tiles_n = voc;
-    d.kb_total = (C + kKB - 1) / kKB;
-  } else if (j.kind == JOB_DX) {
-    d.tiles_m = rows;
-    d.tiles_n = cols;
-    d.kb_total = (j.vn + kKB - 1) / kKB;
-  } else {
-    d.tiles_m = voc;
-    d.tiles_n = cols;
-    d.kb_total = (kept + kKB - 1) / kKB;
-  }
-  d.kb_per = d.kb_total;
-  if (j.kind == JOB_DX) {
-    split_dx(d.tiles_m * d.tiles_n, kb_first, d.splits, d.kb_per);
-    d.splits = (d.kb_total + d.kb_per - 1) / d.kb_per;
-  }
-  d.units = d.tiles_m * d.tiles_n * d.splits;
-  return d;
-}
-
 // Rows of one dx accumulator (a multiple of the tile).
 __host__ __device__ inline int slot_rows(int kept) { return (kept + kTile - 1) / kTile * kTile; }
 
-struct Unit {
-  int job, tm, tn, split, kb0, nkb;
+// The units of a call, for `kept` rows.
+struct Sched {
+  int pieces, piece, V;
+  int tm, tc;          // tiles of kept rows, of C
+  int kb_c, kb_n;      // K blocks of the logits, of dW
+  int splits, kb_per;  // of dx over a whole piece
+  __host__ __device__ int cols(int p) const { return p + 1 < pieces ? piece : V - p * piece; }
+  __host__ __device__ int tv(int p) const { return (cols(p) + kTile - 1) / kTile; }
+  __host__ __device__ int kb_v(int p) const { return (cols(p) + kKB - 1) / kKB; }
+  // a shorter last piece keeps the parts' length: it adds into accumulators
+  // that the first piece has written
+  __host__ __device__ int splits_of(int p) const { return (kb_v(p) + kb_per - 1) / kb_per; }
+  __host__ __device__ int dz(int p) const { return tm * tv(p); }
+  __host__ __device__ int dw(int p) const { return tv(p) * tc; }
+  __host__ __device__ int dx(int p) const { return tm * tc * splits_of(p); }
 };
-
-// Unit u of the launch. Within a job units go through bands of kBand row
-// tiles, columns within a band, rows fastest: the 74 pairs then work on about
-// 8 x 9 tiles at a time, whose operands (17 x 256 rows of K) come from L2.
-constexpr int kBand = 8;
-__device__ __forceinline__ bool find_unit(int u, int n_jobs, const Dims* dims, Unit& o) {
-  for (int j = 0; j < n_jobs; ++j) {
-    const Dims& d = dims[j];
-    if (u >= d.units) {
-      u -= d.units;
-      continue;
-    }
-    const int tiles = d.tiles_m * d.tiles_n;
-    o.job = j;
-    o.split = u / tiles;
-    int r = u - o.split * tiles;
-    const int band = r / (kBand * d.tiles_n);
-    r -= band * kBand * d.tiles_n;
-    const int h = min(kBand, d.tiles_m - band * kBand);
-    o.tn = r / h;
-    o.tm = band * kBand + r - o.tn * h;
-    o.kb0 = o.split * d.kb_per;
-    o.nkb = min(d.kb_total, o.kb0 + d.kb_per) - o.kb0;
-    return true;
-  }
-  return false;
+__host__ __device__ inline Sched make_sched(const Params& p, int kept) {
+  Sched s;
+  s.pieces = p.pieces;
+  s.piece = p.piece;
+  s.V = p.V;
+  s.tm = (kept + kTile - 1) / kTile;
+  s.tc = (p.C + kTile - 1) / kTile;
+  s.kb_c = (p.C + kKB - 1) / kKB;
+  s.kb_n = (kept + kKB - 1) / kKB;
+  split_dx(s.tm * s.tc, s.kb_v(0), s.splits, s.kb_per);
+  return s;
 }
 
+struct __align__(16) Unit {
+  int kind, p, tm, tn, split, kb0, nkb, pad;
+};
+
+// Tile r of tiles_m x tiles_n: bands of `high` row tiles, columns within a
+// band, rows fastest. Bands of 8 let the 74 pairs work on about 8 x 9 tiles at a
+// time, whose operands (17 x 256 rows of K) come from L2; the logits take bands
+// of 32, whose rows of x stay in L2 while W passes once per band.
+constexpr int kBand = 8, kLogitsBand = 32;
+__device__ __forceinline__ void band_tile(int r, int tiles_m, int tiles_n, int high, int& tm,
+                                          int& tn) {
+  const int band = r / (high * tiles_n);
+  r -= band * high * tiles_n;
+  const int h = min(high, tiles_m - band * high);
+  tn = r / h;
+  tm = band * high + r - tn * h;
+}
+
+// Unit u in the order above; kind END past the last one.
+template <bool kBwd>
+__device__ __forceinline__ Unit find_unit(const Sched& s, int u) {
+  Unit o = {};
+  o.kind = END;
+  auto logits = [&](int kind, int p) {
+    o.kind = kind;
+    o.p = p;
+    o.nkb = s.kb_c;
+    band_tile(u, s.tm, s.tv(p), kLogitsBand, o.tm, o.tn);
+  };
+  if constexpr (!kBwd) {
+    if (u < s.dz(0)) logits(LSE, 0);
+    return o;
+  }
+  for (int p = 0; p < min(2, s.pieces); ++p) {
+    if (u < s.dz(p)) {
+      logits(DZ, p);
+      return o;
+    }
+    u -= s.dz(p);
+  }
+  // groups of whole pieces have one size
+  const int group = s.dw(0) + s.dx(0) + s.dz(0);
+  int p = s.pieces > 3 ? min(u / group, s.pieces - 3) : 0;
+  u -= p * group;
+  for (; p < s.pieces; ++p) {
+    if (u < s.dw(p)) {
+      o.kind = DW;
+      o.p = p;
+      o.nkb = s.kb_n;
+      band_tile(u, s.tv(p), s.tc, kBand, o.tm, o.tn);
+      return o;
+    }
+    u -= s.dw(p);
+    if (u < s.dx(p)) {
+      o.kind = DX;
+      o.p = p;
+      const int tiles = s.tm * s.tc;
+      o.split = u / tiles;
+      band_tile(u - o.split * tiles, s.tm, s.tc, kBand, o.tm, o.tn);
+      o.kb0 = o.split * s.kb_per;
+      o.nkb = min(s.kb_v(p), o.kb0 + s.kb_per) - o.kb0;
+      return o;
+    }
+    u -= s.dx(p);
+    if (p + 2 < s.pieces) {
+      if (u < s.dz(p + 2)) {
+        logits(DZ, p + 2);
+        return o;
+      }
+      u -= s.dz(p + 2);
+    }
+  }
+  return o;
+}
+
+// ---- instructions this kernel adds to sm100.cuh's ----
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
   asm volatile(
       "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
@@ -204,7 +254,18 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y,
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
 }
-
+// Into the shared memory of either CTA of the pair (an address of map_rank).
+__device__ __forceinline__ void st_cluster_v4(uint32_t a, int x, int y, int z, int w) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z),
+               "r"(w)
+               : "memory");
+}
+// Arrive on a barrier of either CTA (an address of map_rank) for reads that are
+// done: no release at cluster scope, which first waits for all that the warp
+// has in flight (2800 cycles per unit in the MMA warp, whose products drained).
+__device__ __forceinline__ void mbar_arrive_read(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(
@@ -224,6 +285,51 @@ __device__ __forceinline__ void mma_pair_if(uint32_t issue, uint32_t d_tmem, uin
       "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
       : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+__device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void red_release(unsigned* p, unsigned v) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// A warp's bounded wait, one answer for all of its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+__device__ __forceinline__ bool warp_wait_cl(uint32_t bar, uint32_t parity,
+                                             volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait_cl(bar, parity, abort_flag));
+}
+
+// Bounded wait for a counter of ctl, then for loads by TMA of what was written
+// before it was raised.
+__device__ __forceinline__ bool wait_count(const unsigned* c, unsigned want,
+                                           volatile int* abort_flag) {
+  if (ld_acquire(c) < want) {
+    const long long t0 = clock64();
+    while (ld_acquire(c) < want) {
+      if (*abort_flag) return false;
+      if (clock64() - t0 > kWaitLimitCycles) {
+        *abort_flag = 1;
+        report_status(ATTN_ETIMEOUT);
+        return false;
+      }
+      __nanosleep(100);
+    }
+  }
+  fence_proxy_async();
+  return true;
+}
+
+__device__ __forceinline__ bool warp_count(const unsigned* c, unsigned want,
+                                           volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait_count(c, want, abort_flag));
 }
 
 // 128 rows (K contiguous: row0.., K from k0) or 128 columns (row index
@@ -245,7 +351,16 @@ __device__ __forceinline__ void load_operand(const CUtensorMap* m, bool mn, bool
 struct Named {
   const int* ids;
   int K, pos, next;
-  __device__ __forceinline__ void start(const int* row_ids, int k, int col) {
+  __device__ __forceinline__ void none() {
+    K = pos = 0;
+    next = INT_MAX;
+  }
+  __device__ __forceinline__ void one(int id, int col) {
+    K = 1;
+    pos = 0;
+    next = id >= col ? id : INT_MAX;
+  }
+  __device__ __forceinline__ void list(const int* row_ids, int k, int col) {
     ids = row_ids;
     K = k;
     int lo = 0, hi = k;
@@ -257,23 +372,21 @@ struct Named {
     pos = lo;
     next = lo < k ? ids[lo] : INT_MAX;
   }
-  __device__ __forceinline__ void none() {
-    K = pos = 0;
-    next = INT_MAX;
-  }
   __device__ __forceinline__ void advance() {
     ++pos;
     next = pos < K ? ids[pos] : INT_MAX;
   }
 };
 
+// kBwd: the backward's units, else the forward's. Two kernels, so that neither
+// carries the other's epilogues.
+template <bool kBwd>
 __global__ void __launch_bounds__(kThreads, 1)
     head_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t sb0 = smem_u32(smem_raw);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + kSmMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + kSmMisc + 4);
-  Dims* dims = reinterpret_cast<Dims*>(smem_raw + kSmJobs);
   auto bar = [&](int i) -> uint32_t { return sb0 + kSmBars + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
@@ -293,8 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(bAccFull + a), 1);
       mbar_init(bar(bAccEmpty + a), 2 * kEpiWarps);  // the epilogue warps of both CTAs
     }
+    for (int t = 0; t < kTickets; ++t) {
+      mbar_init(bar(bTkFull + t), 1);
+      // readers: the epilogue and TMA warps of both CTAs, CTA 0's MMA warp
+      mbar_init(bar(bTkEmpty + t), 2 * kEpiWarps + 3);
+    }
     *abort_flag = 0;
-    for (int j = 0; j < p.n_jobs; ++j) dims[j] = job_dims(p.job[j], kept, p.C, p.kb_first);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -306,7 +423,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync_all();  // both CTAs' barriers ready before cross-CTA signals
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int u0 = (int)blockIdx.x >> 1, ustep = (int)gridDim.x >> 1;
+
+  // Unit n of this pair (every reader of the ring calls it once per n). The
+  // forward's units are all alike and wait for nothing: they are dealt in turn,
+  // which measured 3 % (C = 2048) and 6 % (C = 768) faster than taking numbers.
+  const Sched sc = make_sched(p, kept);
+  auto next_unit = [&](int n, Unit& un) -> bool {
+    if constexpr (!kBwd) {
+      un = find_unit<kBwd>(sc, (int)(blockIdx.x >> 1) + n * (int)(gridDim.x >> 1));
+      return un.kind != END;
+    }
+    const int t = n % kTickets;
+    if (!warp_wait_cl(bar(bTkFull + t), (n / kTickets) & 1, abort_flag)) return false;
+    const int4* src = reinterpret_cast<const int4*>(smem_raw + kSmTickets + t * 32);
+    const int4 a = src[0], b = src[1];
+    un.kind = a.x;
+    un.p = a.y;
+    un.tm = a.z;
+    un.tn = a.w;
+    un.split = b.x;
+    un.kb0 = b.y;
+    un.nkb = b.z;
+    const bool more = __any_sync(0xffffffffu, un.kind != END);  // every lane has its values
+    if (lane == 0) mbar_arrive_read(map_rank(bar(bTkEmpty + t), 0));
+    return more;
+  };
+  unsigned* const dz_done = p.ctl + kCtlPieces;
+  unsigned* const dz_used = dz_done + p.pieces;
+  unsigned* const dx_done = dz_used + p.pieces;
 
   // The TMA and MMA warps run their loops converged, one elected lane issuing:
   // the operands of the issue then live in uniform registers. Issued from a
@@ -318,30 +462,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool all = kept == p.N;  // every row kept: x is read in place
     int s = 0;
     uint32_t phase = 1;  // a fresh barrier's previous phase counts as complete
+    int dz_ok = -1, used_ok = -1, dx_ok = -1;  // pieces whose counters are known to be full
     bool ok = true;
     Unit un;
-    for (int u = u0; ok && find_unit(u, p.n_jobs, dims, un); u += ustep) {
-      const Job& j = p.job[un.job];
+    for (int n = 0; ok && next_unit(n, un); ++n) {
       const CUtensorMap *ma, *mb;
       bool a_mn = false, b_mn = true, b_one = p.c_blocks != 0;
+      const int v0 = un.p * p.piece, buf = un.p % kDzBuffers;
       int bk = 0, brow = un.tn * kTile + rank * 128;
-      if (j.kind <= JOB_DZ) {
+      const int arow = un.tm * kTile + rank * 128;
+      if (!kBwd || un.kind == DZ) {
         ma = all ? &maps.x_k : &maps.xc_k;
         mb = &maps.w_k;
         b_mn = false;
-        brow += j.v0;
-      } else if (j.kind == JOB_DX) {
-        ma = &maps.dz_k[j.buf];
-        mb = &maps.w_mn;
-        bk = j.v0;
+        brow += v0;
+        const int q = un.p - kDzBuffers;  // the piece whose dz this one overwrites
+        if (q > used_ok) {
+          if (!warp_count(dz_used + q, 2u * (sc.dw(q) + sc.dx(q)), abort_flag)) break;
+          used_ok = q;
+        }
       } else {
-        ma = &maps.dz_mn[j.buf];
-        mb = all ? &maps.x_mn : &maps.xc_mn;
-        a_mn = true;
+        if (un.kind == DX) {
+          ma = &maps.dz_k[buf];
+          mb = &maps.w_mn;
+          bk = v0;
+        } else {
+          ma = &maps.dz_mn[buf];
+          mb = all ? &maps.x_mn : &maps.xc_mn;
+          a_mn = true;
+        }
+        if (un.p > dz_ok) {
+          if (!warp_count(dz_done + un.p, 2u * kEpiWarps * sc.dz(un.p), abort_flag)) break;
+          dz_ok = un.p;
+        }
+        if (un.kind == DX && un.p - 1 > dx_ok) {
+          if (!warp_count(dx_done + un.p - 1, 2u * kEpiWarps * sc.dx(un.p - 1), abort_flag)) break;
+          dx_ok = un.p - 1;
+        }
       }
-      const int arow = un.tm * kTile + rank * 128;
       for (int kb = 0; kb < un.nkb; ++kb) {
-        if (!mbar_wait(bar(bEmpty + s), phase, abort_flag)) {
+        if (!warp_wait(bar(bEmpty + s), phase, abort_flag)) {
           ok = false;
           break;
         }
@@ -367,13 +527,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t el = elect_one() ? 1u : 0u;
       const uint64_t k_desc = smem_desc_sw128(sb0 + kSmRing, 16, 1024);
       const uint64_t mn_desc = smem_desc_sw128(sb0 + kSmRing, 8192, 1024);
-      int s = 0, n = 0;
+      int s = 0;
       uint32_t phase = 0;
       bool ok = true;
       Unit un;
-      for (int u = u0; ok && find_unit(u, p.n_jobs, dims, un); u += ustep, ++n) {
-        const int kind = p.job[un.job].kind;
-        const bool a_mn = kind == JOB_DW, b_mn = kind >= JOB_DX;
+      ok = next_unit(0, un);
+      for (int n = 0; ok; ++n) {
+        const bool a_mn = kBwd && un.kind == DW, b_mn = kBwd && un.kind >= DX;
         const uint32_t idesc = idesc_f16(kTile, kTile, true, true, a_mn, b_mn);
         // descriptors count in 16 bytes: 16 K values are 32 bytes along a row
         // of K, or 16 rows of 128 bytes
@@ -381,12 +541,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t b0 = (b_mn ? mn_desc : k_desc) + (kOperandBytes >> 4);
         const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;
         const int a = n & 1;
-        if (n >= 2 && !mbar_wait_cl(bar(bAccEmpty + a), ((n >> 1) - 1) & 1, abort_flag)) break;
+        if (n >= 2 && !warp_wait_cl(bar(bAccEmpty + a), ((n >> 1) - 1) & 1, abort_flag)) break;
         tc_fence_after();
         const uint32_t acc = tmem + a * kTile;
         uint32_t on = 0;
         for (int kb = 0; kb < un.nkb; ++kb) {
-          if (!mbar_wait_cl(bar(bFull + s), phase, abort_flag)) {
+          if (!warp_wait_cl(bar(bFull + s), phase, abort_flag)) {
             ok = false;
             break;
           }
@@ -405,18 +565,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             phase ^= 1;
           }
         }
-        if (ok && el) commit_pair(bar(bAccFull + a));
+        if (!ok) break;
+        if (el) commit_pair(bar(bAccFull + a));
         __syncwarp();
+        ok = next_unit(n + 1, un);
       }
+    }
+  } else if (warp == 2 + kEpiWarps && rank == 0) {
+    // ---------------- hand-out of units to both CTAs ----------------
+    // A warp of its own: taking a number and finding its unit are long chains
+    // that would hold up the loads.
+    for (int n = 0; kBwd; ++n) {
+      const int t = n % kTickets;
+      if (!warp_wait_cl(bar(bTkEmpty + t), ((n / kTickets) & 1) ^ 1, abort_flag)) break;
+      unsigned u = 0;
+      if (lane == 0) u = atomicAdd(p.ctl, 1u);
+      const Unit un = find_unit<kBwd>(sc, (int)__shfl_sync(0xffffffffu, u, 0));
+      if (lane < 2) {
+        const uint32_t dst = map_rank(sb0 + kSmTickets + t * 32, lane);
+        st_cluster_v4(dst, un.kind, un.p, un.tm, un.tn);
+        st_cluster_v4(dst + 16, un.split, un.kb0, un.nkb, 0);
+        mbar_arrive_remote(map_rank(bar(bTkFull + t), lane));
+      }
+      __syncwarp();
+      if (un.kind == END) break;
     }
   } else if (warp == 2 + kEpiWarps) {
     // ---------------- the target's logit ----------------
     // A single named id per row is a dot product of its own, in plain fp32: the
     // loss is the difference lse - z, and the tensor core's sums, cut instead
     // of rounded, would leave about 1e-6 of it. Runs beside the products.
-    if (p.n_jobs == 1 && p.job[0].kind == JOB_LSE && !p.share) {
+    if (!kBwd && !p.share) {
       const int c8 = p.C / 8;
-      for (int m = blockIdx.x; m < kept; m += gridDim.x) {
+      for (int m = blockIdx.x >> 1; m < kept; m += gridDim.x >> 1) {
         const int row = p.row_of[m];
         const uint4* xr = p.x + (size_t)row * c8;
         const uint4* wr = p.w + (size_t)p.ids[row] * c8;
@@ -440,53 +621,83 @@ __global__ void __launch_bounds__(kThreads, 1)
     // warp w reads lanes 32 (w % 4).. of columns 128 half..: two warps per lane quarter
     const int sub = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16) + half * 128;
-    const uint32_t stage = sb0 + kSmStage + (warp - 2) * 4096;
-    const uint32_t my_row = stage + lane * 128;
+    uint32_t stage = sb0 + kSmStage + (warp - 2) * 8192;  // of the two buffers, the next one
     const int sw = lane & 7;
     const float c2 = p.inv_tau * kLog2e;
-    int n = 0;
+    // the counter that this warp's stores of its last unit will raise (lane 0)
+    unsigned* owed = nullptr;
+    // staging is free again, and the stores are complete: raise what they owe
+    auto settle = [&]() {
+      if (lane == 0) {
+        bulk_wait_group0();
+        if (owed) {
+          fence_proxy_async();
+          red_release(owed, 1u);
+          owed = nullptr;
+        }
+      }
+      __syncwarp();
+    };
+    auto reuse_stage = [&]() {  // the next buffer is free again
+      if (lane == 0) bulk_wait_group_read1();
+      __syncwarp();
+    };
     Unit un;
-    for (int u = u0; find_unit(u, p.n_jobs, dims, un); u += ustep, ++n) {
-      const Job& j = p.job[un.job];
+    RowPar rp = {0.f, 0.f, 0.f, 0};
+    auto fetch_row = [&](const Unit& w) {
+      const int m = w.tm * kTile + rank * 128 + sub * 32 + lane;
+      if (w.kind <= DZ && m < kept) rp = p.par[m];
+    };
+    bool more = next_unit(0, un);
+    if (more) fetch_row(un);
+    for (int n = 0; more; ++n) {
       const int a = n & 1;
       const int row0 = un.tm * kTile + rank * 128 + sub * 32;  // of this warp
       const int m = row0 + lane;
-      const int col0 = un.tn * kTile + half * 128;  // within the job's columns
-      // what the row needs is fetched while the main loop still runs
+      const int col0 = un.tn * kTile + half * 128;  // within the piece, or of C
+      const int v0 = un.p * p.piece, vn = min(p.piece, p.V - v0), vend = v0 + vn;
+      // the row's named ids, while the main loop still runs
       Named nm;
       nm.none();
-      float lse2 = 0.f, ca = 0.f, cb = 0.f;
       const float* share = nullptr;
-      if (j.kind <= JOB_DZ && m < kept) {
-        const int row = p.row_of[m];
-        // the forward's single target has a warp of its own
-        if (j.kind == JOB_DZ || p.share) nm.start(p.ids + (size_t)row * p.K, p.K, j.v0 + col0);
-        if (j.kind == JOB_DZ) {
-          lse2 = p.lse[row] * kLog2e;
-          const float g = p.dloss[row];
-          ca = (g + (p.dlse ? p.dlse[row] : 0.f)) * p.inv_tau;
-          cb = g * p.inv_tau;
-          if (p.share) share = p.share + (size_t)row * p.K;
+      float lse2 = 0.f, ca = 0.f, cb = 0.f;
+      if (un.kind <= DZ && m < kept) {
+        if (p.share) {
+          nm.list(p.ids + (size_t)rp.id * p.K, p.K, v0 + col0);
+          share = p.share + (size_t)rp.id * p.K;
+        } else if (un.kind == DZ) {  // the forward's single target has a warp of its own
+          nm.one(rp.id, v0 + col0);
         }
+        lse2 = rp.lse2;
+        ca = rp.ca;
+        cb = rp.cb;
       }
-      if (!mbar_wait(bar(bAccFull + a), (n >> 1) & 1, abort_flag)) break;
+      const uint32_t full = bar(bAccFull + a), par = (n >> 1) & 1;
+      if (!__all_sync(0xffffffffu, mbar_test(full, par))) settle();  // others may wait for it: never block owing
+      if (!warp_wait(full, par, abort_flag)) break;
       tc_fence_after();
+      // the next unit, so that its rows' values arrive during this one
+      Unit nu;
+      more = next_unit(n + 1, nu);
+      if (more) fetch_row(nu);
       auto release = [&]() {
         // every column of this accumulator that this warp uses has been read
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(map_rank(bar(bAccEmpty + a), 0));
+        if (lane == 0) mbar_arrive_read(map_rank(bar(bAccEmpty + a), 0));
       };
-      const int vend = j.v0 + j.vn;  // columns of the logits stop here
-      if (j.kind == JOB_LSE) {
+      const uint32_t src = tl + a * kTile;
+      if constexpr (!kBwd) {
         float mx = -INFINITY, sum = 0.f;
-#pragma unroll 1
+        uint32_t v[2][32];
+        tmem_ld32(src, v[0]);
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tmem_ld32(tl + a * kTile + 32 * c, v);
           tmem_wait_ld();
-          if (c == 3) release();
-          const int cc = j.v0 + col0 + 32 * c;
+          if (c < 3) tmem_ld32(src + 32 * (c + 1), v[(c + 1) & 1]);
+          else release();
+          const uint32_t* t = v[c & 1];
+          const int cc = v0 + col0 + 32 * c;
           // named logits of this chunk, one column at a time for the warp
           while (true) {
             const int hit = __reduce_min_sync(0xffffffffu, nm.next);
@@ -494,54 +705,66 @@ __global__ void __launch_bounds__(kThreads, 1)
             float z = 0.f;
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (hit == cc + e) z = __uint_as_float(v[e]);
+              if (hit == cc + e) z = __uint_as_float(t[e]);
             while (nm.next == hit) {
               p.named[(size_t)m * p.K + nm.pos] = z * p.inv_tau;
               nm.advance();
             }
           }
-          float t[32];
+          float f[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) t[e] = __uint_as_float(v[e]) * c2;
+          for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(t[e]);
           if (cc + 32 > vend) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (cc + e >= vend) t[e] = -INFINITY;
+              if (cc + e >= vend) f[e] = -INFINITY;
           }
-          float cm = t[0];
+          float cm = max3f(f[0], f[1], f[2]);
 #pragma unroll
-          for (int e = 1; e < 31; e += 2) cm = max3f(cm, t[e], t[e + 1]);
-          cm = fmaxf(cm, t[31]);
+          for (int e = 3; e < 31; e += 2) cm = max3f(cm, f[e], f[e + 1]);
+          cm = fmaxf(cm, f[31]) * c2;
           const float nx = fmaxf(mx, cm);
           if (nx > -INFINITY) {
-            float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+            const float2 k2 = make_float2(c2, c2), n2 = make_float2(-nx, -nx);
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              s0 += ex2(t[e] - nx);
-              s1 += ex2(t[e + 1] - nx);
-              s2 += ex2(t[e + 2] - nx);
-              s3 += ex2(t[e + 3] - nx);
+              const float2 x0 = __ffma2_rn(make_float2(f[e], f[e + 1]), k2, n2);
+              const float2 x1 = __ffma2_rn(make_float2(f[e + 2], f[e + 3]), k2, n2);
+              s0 = __fadd2_rn(s0, make_float2(ex2(x0.x), ex2(x0.y)));
+              s1 = __fadd2_rn(s1, make_float2(ex2(x1.x), ex2(x1.y)));
             }
-            sum = sum * ex2(mx - nx) + ((s0 + s1) + (s2 + s3));
+            sum = sum * ex2(mx - nx) + ((s0.x + s0.y) + (s1.x + s1.y));
             mx = nx;
           } else {
             // only -inf or NaN so far: NaN has to stay
 #pragma unroll
-            for (int e = 0; e < 32; ++e) sum += t[e] == -INFINITY ? 0.f : t[e];
+            for (int e = 0; e < 32; ++e) sum += f[e] == -INFINITY ? 0.f : f[e];
           }
         }
         if (m < kept) p.part[(size_t)(2 * un.tn + half) * p.row_pitch + m] = make_float2(mx, sum);
-      } else if (j.kind == JOB_DZ) {
-#pragma unroll 1
+      } else if (un.kind == DZ) {
+        const int buf = un.p % kDzBuffers;
+        uint32_t v[2][32];
+        tmem_ld32(src, v[0]);
+        const float2 k2 = make_float2(c2, c2), l2 = make_float2(-lse2, -lse2),
+                     a2 = make_float2(ca, ca);
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tmem_ld32(tl + a * kTile + 32 * c, v);
           tmem_wait_ld();
-          if (c == 3) release();
-          const int cc = j.v0 + col0 + 32 * c;
+          if (c < 3) tmem_ld32(src + 32 * (c + 1), v[(c + 1) & 1]);
+          else release();
+          const uint32_t* tv = v[c & 1];
+          const int cc = v0 + col0 + 32 * c;
           float t[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) t[e] = ca * ex2(fmaf(__uint_as_float(v[e]), c2, -lse2));
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x =
+                __ffma2_rn(make_float2(__uint_as_float(tv[e]), __uint_as_float(tv[e + 1])), k2, l2);
+            const float2 y = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), a2);
+            t[e] = y.x;
+            t[e + 1] = y.y;
+          }
           while (true) {
             const int hit = __reduce_min_sync(0xffffffffu, nm.next);
             if (hit >= cc + 32) break;
@@ -563,10 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e)
               if (e >= left) t[e] = 0.f;
           }
-          if ((c & 1) == 0) {
-            if (lane == 0) bulk_wait_group_read0();  // the staging buffer is free again
-            __syncwarp();
-          }
+          if (c == 0) settle();
+          const uint32_t my_row = stage + lane * 128;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             st_shared_v4(my_row + ((((c & 1) * 4 + e) ^ sw) << 4), pack_bf16(t[8 * e], t[8 * e + 1]),
@@ -576,31 +797,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&maps.dz_out[j.buf], stage, col0 + 32 * (c - 1), row0);
+              tma_store_2d(&maps.dz_out[buf], stage, col0 + 32 * (c - 1), row0);
               bulk_commit_group();
             }
+            stage ^= 4096;
           }
         }
+        if (lane == 0) owed = dz_done + un.p;
       } else {
-        const bool f32 = j.kind == JOB_DX || p.dw_f32;
-        const CUtensorMap* mo = j.kind == JOB_DX ? &maps.dx_out : &maps.dw_out;
-        const int out_row = j.kind == JOB_DX ? un.split * slot_rows(kept) + row0 : j.v0 + row0;
-        const int out_rows = j.kind == JOB_DX ? kept : j.vn;  // rows of the job that exist
+        // dz of this unit has been read (by the products that this warp waited for)
+        if (warp == 2 && lane == 0) red_release(dz_used + un.p, 1u);
+        const bool is_dx = un.kind == DX;
+        const bool last = un.p + 1 == p.pieces;  // of the vocabulary
+        int splits = 1, kb_per;
+        if (is_dx)
+          split_dx(((kept + kTile - 1) / kTile) * ((p.C + kTile - 1) / kTile),
+                   (min(p.piece, p.V) + kKB - 1) / kKB, splits, kb_per);
+        const bool direct = is_dx && last && splits == 1;  // the sum ends here: straight to dx
+        const bool f32 = is_dx || p.dw_f32;
+        const CUtensorMap* mo = is_dx ? &maps.dx_out : &maps.dw_out;
+        const int slot = slot_rows(kept);
+        const int out_row = is_dx ? un.split * slot + row0 : v0 + row0;
+        const int out_rows = is_dx ? kept : vn;  // rows of the job that exist
+        const int row = is_dx && last && m < kept ? p.row_of[m] : 0;
+        settle();
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
-          tmem_ld32(tl + a * kTile + 32 * c, v);
+          tmem_ld32(src + 32 * c, v);
+          const int cs = col0 + 32 * c;
           tmem_wait_ld();
           if (c == 3) release();
           if (un.nkb == 0) {  // no rows kept: nothing was multiplied
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = 0u;
           }
-          if (col0 + 32 * c >= p.C || row0 >= out_rows) continue;  // uniform in the warp
-          if (f32 || (c & 1) == 0) {
-            if (lane == 0) bulk_wait_group_read0();
-            __syncwarp();
+          if (cs >= p.C || row0 >= out_rows) continue;  // uniform in the warp
+          if (direct) {
+            if (m < kept) {
+              const float4* before = reinterpret_cast<const float4*>(p.acc + (size_t)m * p.C + cs);
+              uint4* out = reinterpret_cast<uint4*>(p.dx + (size_t)row * p.C + cs);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (cs + 8 * e >= p.C) break;  // C % 8 == 0
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * e + i]);
+                if (un.p > 0) {
+                  const float4 x = __ldcg(before + 2 * e), y = __ldcg(before + 2 * e + 1);
+                  f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+                  f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+                }
+                out[e] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                    pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+              }
+            }
+            continue;
           }
+          if (c > 1 && (f32 || (c & 1) == 0)) reuse_stage();
+          const uint32_t my_row = stage + lane * 128;
           if (f32) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -616,21 +871,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                            pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
             }
           }
-          const bool last = col0 + 32 * (c + 1) >= p.C;
-          if (f32 || (c & 1) || last) {
+          if (f32 || (c & 1) || cs + 32 >= p.C) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              const int cs = col0 + 32 * (f32 ? c : (c & ~1));
-              if (j.kind == JOB_DX && j.add) tma_reduce_add_2d(mo, stage, cs, out_row);
-              else tma_store_2d(mo, stage, cs, out_row);
+              const int at = f32 ? cs : col0 + 32 * (c & ~1);
+              if (is_dx && un.p > 0) tma_reduce_add_2d(mo, stage, at, out_row);
+              else tma_store_2d(mo, stage, at, out_row);
               bulk_commit_group();
+            }
+            stage ^= 4096;
+          }
+        }
+        if (is_dx && lane == 0) owed = dx_done + un.p;
+        if (is_dx && last && !direct && col0 < p.C && row0 < kept) {
+          // the last split to finish these 32 x 128 values adds all of them
+          settle();
+          const int tiles_c = (p.C + kTile - 1) / kTile;
+          unsigned* cnt = dx_done + p.pieces +
+                          ((un.tm * tiles_c + un.tn) * 2 + rank) * kEpiWarps + (warp - 2);
+          const int parts = ((vn + kKB - 1) / kKB + kb_per - 1) / kb_per;
+          unsigned before = 0;
+          if (lane == 0) {
+            __threadfence();
+            before = atomicAdd(cnt, 1u);
+            __threadfence();
+          }
+          before = __shfl_sync(0xffffffffu, before, 0);
+          __syncwarp();
+          if (before == (unsigned)(parts - 1)) {
+            const int cl = col0 + 4 * lane;
+            const int rows = min(32, kept - row0);
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r) {
+              const int to = __shfl_sync(0xffffffffu, row, r);
+              if (cl >= p.C) continue;
+              float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+              const float* from = p.acc + (size_t)(row0 + r) * p.C + cl;
+              for (int q = 0; q < splits; ++q, from += (size_t)slot * p.C) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(from));
+                f.x += x.x; f.y += x.y; f.z += x.z; f.w += x.w;
+              }
+              *reinterpret_cast<uint2*>(p.dx + (size_t)to * p.C + cl) =
+                  make_uint2(pack_bf16(f.x, f.y), pack_bf16(f.z, f.w));
             }
           }
         }
       }
+      un = nu;
     }
-    if (lane == 0) bulk_wait_group0();  // stores complete before the CTA ends
+    settle();  // stores complete before the CTA ends
   }
 
   tc_fence_before();

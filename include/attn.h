@@ -385,8 +385,8 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
  *
  * Workspace: attn_head_workspace_bytes(N, V, C, K, is_bwd) bytes, K = 0 for
  * attn_head_ce*; 0 for invalid sizes. The backward takes the vocabulary in
- * pieces, so its workspace does not grow with V: about 2 x 128 MiB for dz plus
- * the fp32 sums of dx. Pure host function.
+ * pieces, so its workspace does not grow with V: about 3 x 96 MiB for dz (up
+ * to 24576 rows) plus the fp32 sums of dx. Pure host function.
  */
 size_t attn_head_workspace_bytes(int N, int V, int C, int K, int is_bwd);
 int attn_head_ce(const void* x, const void* w, const int32_t* target, float* loss, float* lse,
