@@ -17,11 +17,11 @@ constexpr long kDzMinCols = 2048;
 
 struct HeadPlan {
   int rows_pad = 0, piece = 0, pieces = 0, parts = 0;
-  size_t n_kept = 0, ctl = 0, row_of = 0, pos = 0, par = 0, xc = 0, ids = 0, share = 0, entropy = 0, flags = 0;
+  size_t n_kept = 0, ctl = 0, row_of = 0, pos = 0, par = 0, xc = 0, ids = 0, share = 0, entropy = 0, flags = 0, first = 0;
   size_t part = 0, named = 0;     // forward
   size_t dz[head100::kDzBuffers] = {}, acc = 0;  // backward
   long acc_rows = 0;
-  int n_ctl = 0;
+  int n_ctl = 0, first_pitch = 0;
   size_t total = 0;
 };
 
@@ -52,7 +52,7 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
   p.pieces = (int)((V + cols - 1) / cols);
   p.piece = (int)(((V + p.pieces - 1) / p.pieces + kTile - 1) / kTile * kTile);
   p.pieces = (V + p.piece - 1) / p.piece;
-  p.n_ctl = kCtlPieces + 3 * p.pieces + kPairs * 2 * kEpiWarps;
+  p.n_ctl = kCtlPieces + 3 * p.pieces;
   p.n_kept = take(4);
   p.ctl = take((size_t)p.n_ctl * 4);
   p.par = take((size_t)p.rows_pad * sizeof(RowPar));
@@ -63,6 +63,8 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
     p.ids = take((size_t)N * K * 4);
     p.share = take((size_t)N * K * 4);
     p.flags = take((size_t)N * 4);
+    p.first_pitch = 2 * ((V + kTile - 1) / kTile) + 1;
+    p.first = take((size_t)N * p.first_pitch * 2);
     if (!bwd) p.entropy = take((size_t)N * 4);
   }
   if (!bwd) {
@@ -188,15 +190,16 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
 
   if (K) {
     const unsigned blocks = (unsigned)std::min<long>((N + kTeacherWarps - 1L) / kTeacherWarps, 148L * 16);
-    const size_t smem = (size_t)kTeacherWarps * K * 4;
+    const size_t smem = (size_t)kTeacherWarps * K * 8;
+    uint16_t* first = (uint16_t*)(ws + hp.first);
     if (c.t_dtype == ATTN_F32)
       ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_teacher_kernel<float>, blocks, 32 * kTeacherWarps, smem, st,
                                                c.t_idx, (const float*)c.t_logit, inv_tau, c.dloss, c.dlse,
-                                               ids, share, entropy, flags, N, V, K));
+                                               ids, share, first, hp.first_pitch, entropy, flags, N, V, K));
     else
       ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_teacher_kernel<__nv_bfloat16>, blocks, 32 * kTeacherWarps, smem, st,
                                                c.t_idx, (const __nv_bfloat16*)c.t_logit, inv_tau, c.dloss, c.dlse,
-                                               ids, share, entropy, flags, N, V, K));
+                                               ids, share, first, hp.first_pitch, entropy, flags, N, V, K));
   }
   RowsArgs ra = {};
   ra.target = K ? nullptr : c.target;
@@ -239,6 +242,8 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   p.pieces = hp.pieces;
   p.ids = K ? ids : c.target;
   p.share = share;
+  p.first = K ? (const uint16_t*)(ws + hp.first) : nullptr;
+  p.first_pitch = hp.first_pitch;
   p.row_pitch = hp.rows_pad;
   if (!head_map(&maps.x_k, c.x, false, N, C, C, 128) ||
       !head_map(&maps.xc_k, xc, false, hp.rows_pad, C, C, 128) ||
@@ -249,8 +254,8 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
     p.part = (float2*)(ws + hp.part);
     p.named = (float*)(ws + hp.named);
     if (int rc = head_gemm<false>(maps, p, st)) return rc;
-    ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_loss_kernel, (unsigned)((N + kLossRows - 1) / kLossRows),
-                                             kLossRows * kLossSlices, 0, st, p.part, p.named, share, entropy,
+    ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_loss_kernel, (unsigned)((N + kLossThreads / 8 - 1) / (kLossThreads / 8)),
+                                             kLossThreads, 0, st, p.part, p.named, share, entropy,
                                              pos, c.loss, c.lse_out, N, p.K, hp.parts, hp.rows_pad));
     return launch_status();
   }
@@ -275,7 +280,12 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
          head_map(&maps.dz_out[b], dz, false, hp.rows_pad, hp.piece, hp.piece, 32);
   }
   if (!ok) return ATTN_ECUDA;
-  return head_gemm<true>(maps, p, st);
+  if (int rc = head_gemm<true>(maps, p, st)) return rc;
+  const long n8 = (long)N * (C / 8);
+  ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_dx_kernel, (unsigned)std::min<long>((n8 + 255) / 256, 148L * 8),
+                                           256, 0, st, p.acc, row_of, n_kept, (uint4*)c.dx, C,
+                                           (std::min(hp.piece, V) + kKB - 1) / kKB));
+  return launch_status();
 }
 
 }  // namespace

@@ -125,22 +125,24 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowsArgs a
 
 // The teacher's list of one row per warp: q = softmax of t / tau over the
 // entries present (0 <= id < V), ids sorted ascending with their q (absent
-// ones last, id INT_MAX, q 0), sum q log q, and whether the row counts (some
-// entry above -inf, and an upstream gradient that is not zero). The sort is by
-// rank (K comparisons per entry): stable, so equal ids keep their order. The
-// maximum is taken off before the division by tau: entries at the type's
-// lowest value then differ by exactly 0.
+// ones last, id INT_MAX, q 0), how many of them lie below each multiple of 128
+// columns, sum q log q, and whether the row counts (some entry above -inf, and
+// an upstream gradient that is not zero). The sort is by rank (K comparisons
+// per entry): stable, so equal ids keep their order. The maximum is taken off
+// before the division by tau: entries at the type's lowest value then differ
+// by exactly 0.
 template <typename TT>
 __global__ void __launch_bounds__(32 * kTeacherWarps)
     head_teacher_kernel(const int* __restrict__ t_idx, const TT* __restrict__ t_logit,
                         float inv_tau, const float* __restrict__ dloss,
                         const float* __restrict__ dlse, int* __restrict__ ids,
-                        float* __restrict__ share, float* __restrict__ entropy,
-                        int* __restrict__ flags, int N, int V, int K) {
+                        float* __restrict__ share, uint16_t* __restrict__ first, int first_pitch,
+                        float* __restrict__ entropy, int* __restrict__ flags, int N, int V, int K) {
   pdl_wait_and_trigger();
   extern __shared__ int smem_teacher[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int* key = smem_teacher + warp * K;
+  int* key = smem_teacher + warp * 2 * K;
+  int* sorted = key + K;
   for (int r = blockIdx.x * kTeacherWarps + warp; r < N; r += gridDim.x * kTeacherWarps) {
     const int* in = t_idx + (size_t)r * K;
     const TT* tl = t_logit + (size_t)r * K;
@@ -177,14 +179,27 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
         if (q != 0.f) ent += q * (d - log_sum);  // NaN stays
       }
       int rank = 0;
+#pragma unroll 4
       for (int i = 0; i < K; ++i) {
         const int other = key[i];
         rank += (other < mine || (other == mine && i < k)) ? 1 : 0;
       }
+      sorted[rank] = mine;
       ids[(size_t)r * K + rank] = mine;
       share[(size_t)r * K + rank] = q;
     }
     ent = warp_sum(ent);
+    __syncwarp();
+    for (int b = lane; b < first_pitch; b += 32) {
+      int lo = 0, hi = K;
+      const long col = 128L * b;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (sorted[mid] < col) lo = mid + 1;
+        else hi = mid;
+      }
+      first[(size_t)r * first_pitch + b] = (uint16_t)lo;
+    }
     if (lane == 0) {
       flags[r] = some && has_weight(dloss, dlse, r) ? 1 : 0;
       if (entropy) entropy[r] = ent;
@@ -193,19 +208,18 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
   }
 }
 
-// lse and loss of every row from the parts of its logits: 32 rows per block,
-// sixteen threads per row. loss = sum_k q_k (log q_k + lse - z_k), for a single
-// target lse - z.
-constexpr int kLossRows = 32, kLossSlices = 16;
-__global__ void __launch_bounds__(kLossRows* kLossSlices)
+// lse and loss of every row from the parts of its logits: four rows per warp
+// (the 32 bytes that their parts share), eight lanes per row. loss =
+// sum_k q_k (log q_k + lse - z_k), for a single target lse - z.
+constexpr int kLossThreads = 128;
+__global__ void __launch_bounds__(kLossThreads)
     head_loss_kernel(const float2* __restrict__ part, const float* __restrict__ named,
                      const float* __restrict__ share, const float* __restrict__ entropy,
                      const int* __restrict__ pos, float* __restrict__ loss,
                      float* __restrict__ lse, int N, int K, int parts, int row_pitch) {
   pdl_wait_and_trigger();
-  __shared__ float s_m[kLossSlices][kLossRows], s_s[kLossSlices][kLossRows];
-  const int tx = threadIdx.x % kLossRows, ty = threadIdx.x / kLossRows;
-  const int r = blockIdx.x * kLossRows + tx;
+  const int lane = threadIdx.x & 31, slice = lane >> 2;
+  const int r = (blockIdx.x * (kLossThreads / 32) + (threadIdx.x >> 5)) * 4 + (lane & 3);
   const int at = r < N ? pos[r] : -1;
   float m = -INFINITY, s = 0.f;
   auto join = [&](float om, float os) {
@@ -215,11 +229,11 @@ __global__ void __launch_bounds__(kLossRows* kLossSlices)
   };
   if (at >= 0) {
     const float2* mine = part + at;
-    for (int j = ty; j < parts; j += 8 * kLossSlices) {
+    for (int j = slice; j < parts; j += 8 * 8) {
       float2 t[8];  // eight loads in flight
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int q = j + i * kLossSlices;
+        const int q = j + 8 * i;
         t[i] = q < parts ? mine[(size_t)q * row_pitch] : make_float2(-INFINITY, 0.f);
       }
       float top = t[0].x;
@@ -232,28 +246,57 @@ __global__ void __launch_bounds__(kLossRows* kLossSlices)
       join(top, sum);
     }
   }
-  s_m[ty][tx] = m;
-  s_s[ty][tx] = s;
-  __syncthreads();
-  if (ty == 0) {
-    for (int j = 1; j < kLossSlices; ++j) join(s_m[j][tx], s_s[j][tx]);
-    s_m[0][tx] = (m + log2f(s)) * kLn2;
+  // the lanes of a row join in pairs; every lane ends with the same bits
+  for (int o = 4; o < 32; o <<= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o);
+    const float nm = fmaxf(m, om);
+    s = nm > -INFINITY
+            ? __fadd_rn(__fmul_rn(s, exp2f(m - nm)), __fmul_rn(os, exp2f(om - nm)))
+            : s + os;
+    m = nm;
   }
-  __syncthreads();
-  const float l = s_m[0][tx];
+  const float l = (m + log2f(s)) * kLn2;
   float d = 0.f;
   if (at >= 0)
-    for (int k = ty; k < K; k += kLossSlices) {
+    for (int k = slice; k < K; k += 8) {
       const float q = share ? share[(size_t)r * K + k] : 1.f;
       if (q != 0.f) d += q * (l - named[(size_t)at * K + k]);
     }
-  s_s[ty][tx] = d;
-  __syncthreads();
-  if (ty == 0 && r < N) {
-    d = 0.f;
-    for (int j = 0; j < kLossSlices; ++j) d += s_s[j][tx];
+  for (int o = 4; o < 32; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  if (slice == 0 && r < N) {
     lse[r] = at >= 0 ? l : 0.f;
     loss[r] = at >= 0 ? (share ? entropy[r] + d : d) : 0.f;
+  }
+}
+
+// dx of the kept rows where its vocabulary axis was split: the accumulators
+// added in order and rounded once. Eight columns per thread. Without a split
+// the last piece's epilogue has written dx, and this pass ends at once.
+__global__ void __launch_bounds__(256)
+    head_dx_kernel(const float* __restrict__ acc, const int* __restrict__ row_of,
+                   const int* __restrict__ n_kept, uint4* __restrict__ dx, int C, int kb_total) {
+  pdl_wait_and_trigger();
+  const int kept = *n_kept;
+  int splits, kb_per;
+  split_dx(((kept + kTile - 1) / kTile) * ((C + kTile - 1) / kTile), kb_total, splits, kb_per);
+  if (splits == 1) return;
+  const size_t slot = (size_t)slot_rows(kept) * C;
+  const int c8 = C / 8;
+  const long n = (long)kept * c8;
+  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256) {
+    const int m = (int)(i / c8), c = (int)(i - (long)m * c8) * 8;
+    const float* src = acc + (size_t)m * C + c;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s, src += slot) {
+      const float4 a = *reinterpret_cast<const float4*>(src);
+      const float4 b = *reinterpret_cast<const float4*>(src + 4);
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+    dx[(size_t)row_of[m] * c8 + c / 8] =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                   pack_bf16(v[6], v[7]));
   }
 }
 

@@ -96,27 +96,29 @@ struct Params {
   const int* n_kept;     // rows kept (device)
   const int* row_of;     // kept row -> row
   const RowPar* par;     // by kept row
-  const int* ids;        // [N][K] ascending; a negative or >= V id matches nothing
+  const int* ids;        // [N][K]: the targets, or a teacher's ids, ascending
   const float* share;    // [N][K] q, or null (1 at the target)
+  const uint16_t* first; // [N][first_pitch] entries with an id below 128 b (with share)
+  int first_pitch;
   float2* part;          // LSE: [2 tiles][row_pitch] maximum (base 2), sum
   float* named;          // LSE: [kept row][K] z at the row's ids
   int row_pitch;
   const float* acc;      // fp32 sums of dx, slot_rows(kept) rows per split
   __nv_bfloat16* dx;
   // zero at launch: [0] the next unit; then per piece finished dz, consumed dz,
-  // finished dx; then finished splits per warp region of the last piece's dx
+  // finished dx
   unsigned* ctl;
 };
 constexpr int kCtlPieces = 4;  // first per-piece counter in ctl, three per piece
 
 // dx has few tiles when few rows are kept: its K axis (the vocabulary) is
-// then split over units, each with an accumulator of its own that the last one
-// to finish adds in order (whoever that is: results repeat). Two units per CTA
+// then split over units, each with an accumulator of its own that a closing
+// pass adds in order (no atomics on values: results repeat). One unit per CTA
 // pair, at least eight K blocks each.
 __host__ __device__ inline void split_dx(int tiles, int kb_total, int& splits, int& kb_per) {
   splits = 1;
   if (tiles > 0 && tiles < kPairs) {
-    splits = (2 * kPairs + tiles - 1) / tiles;
+    splits = (kPairs + tiles - 1) / tiles;
     const int most = kb_total / 8 > 1 ? kb_total / 8 : 1;
     splits = splits < most ? splits : most;
   }
@@ -254,6 +256,14 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y,
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
 }
+__device__ __forceinline__ float ld_shared_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t a, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
 // Into the shared memory of either CTA of the pair (an address of map_rank).
 __device__ __forceinline__ void st_cluster_v4(uint32_t a, int x, int y, int z, int w) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z),
@@ -346,35 +356,27 @@ __device__ __forceinline__ void load_operand(const CUtensorMap* m, bool mn, bool
   }
 }
 
-// The row's named ids from column col on: position of the first one and its
-// column (INT_MAX when there is none).
+// A teacher's list of one row, from the entry that the current 128 columns
+// begin with; `next` is the id there (INT_MAX past the last one of these
+// columns) and the one behind it is already on its way.
 struct Named {
   const int* ids;
-  int K, pos, next;
+  int pos, end, next, then;
   __device__ __forceinline__ void none() {
-    K = pos = 0;
-    next = INT_MAX;
+    pos = end = 0;
+    next = then = INT_MAX;
   }
-  __device__ __forceinline__ void one(int id, int col) {
-    K = 1;
-    pos = 0;
-    next = id >= col ? id : INT_MAX;
-  }
-  __device__ __forceinline__ void list(const int* row_ids, int k, int col) {
+  __device__ __forceinline__ void list(const int* row_ids, int from, int to) {
     ids = row_ids;
-    K = k;
-    int lo = 0, hi = k;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (ids[mid] < col) lo = mid + 1;
-      else hi = mid;
-    }
-    pos = lo;
-    next = lo < k ? ids[lo] : INT_MAX;
+    pos = from;
+    end = to;
+    next = from < to ? ids[from] : INT_MAX;
+    then = from + 1 < to ? ids[from + 1] : INT_MAX;
   }
   __device__ __forceinline__ void advance() {
     ++pos;
-    next = pos < K ? ids[pos] : INT_MAX;
+    next = then;
+    then = pos + 1 < end ? ids[pos + 1] : INT_MAX;
   }
 };
 
@@ -390,13 +392,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) -> uint32_t { return sb0 + kSmBars + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
-  pdl_wait_and_trigger();
   if (sb0 & 1023u) {  // uniform across the cluster: nothing has been issued yet
     if (threadIdx.x == 0) report_status(ATTN_ECUDA_LAYOUT);
     return;
   }
-  const int kept = *p.n_kept;
-
+  // set up before waiting for the row pass: nothing here touches global memory
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(bFull + s), 1);
@@ -423,6 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync_all();  // both CTAs' barriers ready before cross-CTA signals
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait_and_trigger();
+  const int kept = *p.n_kept;
 
   // Unit n of this pair (every reader of the ring calls it once per n). The
   // forward's units are all alike and wait for nothing: they are dealt in turn,
@@ -643,35 +645,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     Unit un;
+    // what the unit's row needs, fetched while the unit before is worked on
     RowPar rp = {0.f, 0.f, 0.f, 0};
+    int n_from = 0, n_to = 0;
     auto fetch_row = [&](const Unit& w) {
       const int m = w.tm * kTile + rank * 128 + sub * 32 + lane;
       if (w.kind <= DZ && m < kept) rp = p.par[m];
     };
+    auto fetch_named = [&](const Unit& w) {
+      n_from = n_to = 0;
+      const int m = w.tm * kTile + rank * 128 + sub * 32 + lane;
+      if (p.share && w.kind <= DZ && m < kept) {
+        const uint16_t* f = p.first + (size_t)rp.id * p.first_pitch +
+                            (w.p * p.piece + w.tn * kTile + half * 128) / 128;
+        n_from = f[0];
+        n_to = f[1];
+      }
+    };
     bool more = next_unit(0, un);
-    if (more) fetch_row(un);
+    if (more) {
+      fetch_row(un);
+      fetch_named(un);
+    }
     for (int n = 0; more; ++n) {
       const int a = n & 1;
       const int row0 = un.tm * kTile + rank * 128 + sub * 32;  // of this warp
       const int m = row0 + lane;
       const int col0 = un.tn * kTile + half * 128;  // within the piece, or of C
       const int v0 = un.p * p.piece, vn = min(p.piece, p.V - v0), vend = v0 + vn;
-      // the row's named ids, while the main loop still runs
       Named nm;
       nm.none();
       const float* share = nullptr;
-      float lse2 = 0.f, ca = 0.f, cb = 0.f;
-      if (un.kind <= DZ && m < kept) {
-        if (p.share) {
-          nm.list(p.ids + (size_t)rp.id * p.K, p.K, v0 + col0);
-          share = p.share + (size_t)rp.id * p.K;
-        } else if (un.kind == DZ) {  // the forward's single target has a warp of its own
-          nm.one(rp.id, v0 + col0);
-        }
-        lse2 = rp.lse2;
-        ca = rp.ca;
-        cb = rp.cb;
+      if (p.share && n_from < n_to) {
+        nm.list(p.ids + (size_t)rp.id * p.K, n_from, n_to);
+        share = p.share + (size_t)rp.id * p.K;
       }
+      const float lse2 = rp.lse2, ca = rp.ca, cb = rp.cb;
+      const int target = rp.id - (v0 + col0);  // without a list: within these columns or not
       const uint32_t full = bar(bAccFull + a), par = (n >> 1) & 1;
       if (!__all_sync(0xffffffffu, mbar_test(full, par))) settle();  // others may wait for it: never block owing
       if (!warp_wait(full, par, abort_flag)) break;
@@ -698,18 +708,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           else release();
           const uint32_t* t = v[c & 1];
           const int cc = v0 + col0 + 32 * c;
-          // named logits of this chunk, one column at a time for the warp
-          while (true) {
-            const int hit = __reduce_min_sync(0xffffffffu, nm.next);
-            if (hit >= cc + 32) break;
-            float z = 0.f;
+          // a teacher's ids among these 32 columns: each lane looks its row's up
+          // in its own 128 bytes of the staging (swizzled in 16-byte groups)
+          if (__any_sync(0xffffffffu, nm.next < cc + 32)) {
+            const uint32_t mine = stage + lane * 128;
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (hit == cc + e) z = __uint_as_float(t[e]);
-            while (nm.next == hit) {
-              p.named[(size_t)m * p.K + nm.pos] = z * p.inv_tau;
+            for (int e = 0; e < 8; ++e)
+              st_shared_v4(mine + ((e ^ sw) << 4), t[4 * e], t[4 * e + 1], t[4 * e + 2], t[4 * e + 3]);
+            while (nm.next < cc + 32) {
+              const int e = nm.next - cc;
+              p.named[(size_t)m * p.K + nm.pos] =
+                  ld_shared_f32(mine + (((e >> 2) ^ sw) << 4) + (e & 3) * 4) * p.inv_tau;
               nm.advance();
             }
+            __syncwarp();
           }
           float f[32];
 #pragma unroll
@@ -765,18 +777,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             t[e] = y.x;
             t[e + 1] = y.y;
           }
-          while (true) {
-            const int hit = __reduce_min_sync(0xffffffffu, nm.next);
-            if (hit >= cc + 32) break;
-            float q = 0.f;
-            while (nm.next == hit) {
-              q += share ? share[nm.pos] : 1.f;
-              nm.advance();
+          if (p.share) {
+            // a teacher's shares, in a staging buffer that no store reads
+            if (__any_sync(0xffffffffu, nm.next < cc + 32)) {
+              if (lane == 0) bulk_wait_group_read0();
+              __syncwarp();
+              const uint32_t mine = (stage ^ 4096) + lane * 128;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                st_shared_v4(mine + ((e ^ sw) << 4), __float_as_uint(t[4 * e]),
+                             __float_as_uint(t[4 * e + 1]), __float_as_uint(t[4 * e + 2]),
+                             __float_as_uint(t[4 * e + 3]));
+              while (nm.next < cc + 32) {
+                const int e = nm.next - cc;
+                const uint32_t at = mine + (((e >> 2) ^ sw) << 4) + (e & 3) * 4;
+                st_shared_f32(at, fmaf(-cb, share[nm.pos], ld_shared_f32(at)));
+                nm.advance();
+              }
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                t[e] = ld_shared_f32(mine + (((e >> 2) ^ sw) << 4) + (e & 3) * 4);
+              __syncwarp();
             }
-            q *= cb;
+          } else if (__any_sync(0xffffffffu, (unsigned)(target - 32 * c) < 32u)) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (hit == cc + e) t[e] -= q;
+              if (target == 32 * c + e) t[e] -= cb;
           }
           // rows that are not kept and columns past the vocabulary are zeros:
           // they are K values of the products that read this buffer
@@ -819,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = slot_rows(kept);
         const int out_row = is_dx ? un.split * slot + row0 : v0 + row0;
         const int out_rows = is_dx ? kept : vn;  // rows of the job that exist
-        const int row = is_dx && last && m < kept ? p.row_of[m] : 0;
+        const int row = direct && m < kept ? p.row_of[m] : 0;
         settle();
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -884,40 +910,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (is_dx && lane == 0) owed = dx_done + un.p;
-        if (is_dx && last && !direct && col0 < p.C && row0 < kept) {
-          // the last split to finish these 32 x 128 values adds all of them
-          settle();
-          const int tiles_c = (p.C + kTile - 1) / kTile;
-          unsigned* cnt = dx_done + p.pieces +
-                          ((un.tm * tiles_c + un.tn) * 2 + rank) * kEpiWarps + (warp - 2);
-          const int parts = ((vn + kKB - 1) / kKB + kb_per - 1) / kb_per;
-          unsigned before = 0;
-          if (lane == 0) {
-            __threadfence();
-            before = atomicAdd(cnt, 1u);
-            __threadfence();
-          }
-          before = __shfl_sync(0xffffffffu, before, 0);
-          __syncwarp();
-          if (before == (unsigned)(parts - 1)) {
-            const int cl = col0 + 4 * lane;
-            const int rows = min(32, kept - row0);
-#pragma unroll 4
-            for (int r = 0; r < rows; ++r) {
-              const int to = __shfl_sync(0xffffffffu, row, r);
-              if (cl >= p.C) continue;
-              float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-              const float* from = p.acc + (size_t)(row0 + r) * p.C + cl;
-              for (int q = 0; q < splits; ++q, from += (size_t)slot * p.C) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(from));
-                f.x += x.x; f.y += x.y; f.z += x.z; f.w += x.w;
-              }
-              *reinterpret_cast<uint2*>(p.dx + (size_t)to * p.C + cl) =
-                  make_uint2(pack_bf16(f.x, f.y), pack_bf16(f.z, f.w));
-            }
-          }
-        }
       }
+      if (more) fetch_named(nu);
       un = nu;
     }
     settle();  // stores complete before the CTA ends
