@@ -201,6 +201,9 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
                                                c.t_idx, (const __nv_bfloat16*)c.t_logit, inv_tau, c.dloss, c.dlse,
                                                ids, share, first, hp.first_pitch, entropy, flags, N, V, K));
   }
+  // A forward of one row tile costs the same for any number of kept rows, and
+  // its rows do not meet: it goes without the row pass (4 of 27 us at one row).
+  const bool whole = !c.bwd && N <= kTile;
   RowsArgs ra = {};
   ra.target = K ? nullptr : c.target;
   ra.flags = flags;
@@ -222,7 +225,8 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   ra.inv_tau = inv_tau;
   const int row_blocks = (int)std::min<long>((N + 15L) / 16, 148L);
   ra.rows_per_block = (N + row_blocks - 1) / row_blocks;
-  ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_rows_kernel, (unsigned)row_blocks, kRowThreads, 0, st, ra));
+  if (!whole)
+    ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_rows_kernel, (unsigned)row_blocks, kRowThreads, 0, st, ra));
   if (launch_status()) return ATTN_ECUDA;
 
   Maps maps = {};
@@ -234,7 +238,7 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   p.C = C;
   p.K = std::max(K, 1);
   p.inv_tau = inv_tau;
-  p.n_kept = n_kept;
+  p.n_kept = whole ? nullptr : n_kept;
   p.row_of = row_of;
   p.par = ra.par;
   p.ctl = ra.ctl;
@@ -256,7 +260,8 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
     if (int rc = head_gemm<false>(maps, p, st)) return rc;
     ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_loss_kernel, (unsigned)((N + kLossThreads / 8 - 1) / (kLossThreads / 8)),
                                              kLossThreads, 0, st, p.part, p.named, share, entropy,
-                                             pos, c.loss, c.lse_out, N, p.K, hp.parts, hp.rows_pad));
+                                             whole ? nullptr : pos, c.target, flags, c.loss, c.lse_out, N,
+                                             V, p.K, hp.parts, hp.rows_pad));
     return launch_status();
   }
 

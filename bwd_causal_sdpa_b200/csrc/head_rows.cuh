@@ -210,17 +210,29 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
 
 // lse and loss of every row from the parts of its logits: four rows per warp
 // (the 32 bytes that their parts share), eight lanes per row. loss =
-// sum_k q_k (log q_k + lse - z_k), for a single target lse - z.
+// sum_k q_k (log q_k + lse - z_k), for a single target lse - z. Without pos no
+// row was left out before: flags or target say which rows count.
 constexpr int kLossThreads = 128;
 __global__ void __launch_bounds__(kLossThreads)
     head_loss_kernel(const float2* __restrict__ part, const float* __restrict__ named,
                      const float* __restrict__ share, const float* __restrict__ entropy,
-                     const int* __restrict__ pos, float* __restrict__ loss,
-                     float* __restrict__ lse, int N, int K, int parts, int row_pitch) {
+                     const int* __restrict__ pos, const int* __restrict__ target,
+                     const int* __restrict__ flags, float* __restrict__ loss,
+                     float* __restrict__ lse, int N, int V, int K, int parts, int row_pitch) {
   pdl_wait_and_trigger();
   const int lane = threadIdx.x & 31, slice = lane >> 2;
   const int r = (blockIdx.x * (kLossThreads / 32) + (threadIdx.x >> 5)) * 4 + (lane & 3);
-  const int at = r < N ? pos[r] : -1;
+  int at = -1;
+  if (r < N) {
+    if (pos) {
+      at = pos[r];
+    } else if (flags) {
+      at = flags[r] ? r : -1;
+    } else {
+      at = (unsigned)target[r] < (unsigned)V ? r : -1;
+      if (target[r] >= V) report_status(ATTN_EDEVICE_INPUT);
+    }
+  }
   float m = -INFINITY, s = 0.f;
   auto join = [&](float om, float os) {
     const float nm = fmaxf(m, om);

@@ -93,6 +93,7 @@ struct Params {
   int c_blocks;          // C % 64 == 0: _mn maps of x and W take both 64-wide blocks in one box
   int dw_f32;
   float inv_tau;
+  // null in a forward of one row tile, which takes all rows as they are
   const int* n_kept;     // rows kept (device)
   const int* row_of;     // kept row -> row
   const RowPar* par;     // by kept row
@@ -317,6 +318,10 @@ __device__ __forceinline__ bool warp_wait_cl(uint32_t bar, uint32_t parity,
   return __all_sync(0xffffffffu, mbar_wait_cl(bar, parity, abort_flag));
 }
 
+__device__ __forceinline__ void red_relaxed(unsigned* p, unsigned v) {
+  asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
 // Bounded wait for a counter of ctl, then for loads by TMA of what was written
 // before it was raised.
 __device__ __forceinline__ bool wait_count(const unsigned* c, unsigned want,
@@ -412,6 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(bTkEmpty + t), 2 * kEpiWarps + 3);
     }
     *abort_flag = 0;
+    prefetch_tensor_map(&maps.x_k);
+    prefetch_tensor_map(&maps.w_k);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait_and_trigger();
-  const int kept = *p.n_kept;
+  const int kept = !kBwd && !p.n_kept ? p.N : *p.n_kept;
 
   // Unit n of this pair (every reader of the ring calls it once per n). The
   // forward's units are all alike and wait for nothing: they are dealt in turn,
@@ -600,9 +607,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!kBwd && !p.share) {
       const int c8 = p.C / 8;
       for (int m = blockIdx.x >> 1; m < kept; m += gridDim.x >> 1) {
-        const int row = p.row_of[m];
+        const int row = p.n_kept ? p.row_of[m] : m;
+        const int id = p.ids[row];
+        if ((unsigned)id >= (unsigned)p.V) continue;
         const uint4* xr = p.x + (size_t)row * c8;
-        const uint4* wr = p.w + (size_t)p.ids[row] * c8;
+        const uint4* wr = p.w + (size_t)id * c8;
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll 4
         for (int i = lane; i < c8; i += 32) {
@@ -650,7 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n_from = 0, n_to = 0;
     auto fetch_row = [&](const Unit& w) {
       const int m = w.tm * kTile + rank * 128 + sub * 32 + lane;
-      if (w.kind <= DZ && m < kept) rp = p.par[m];
+      if (!kBwd && !p.n_kept) rp.id = m;
+      else if (w.kind <= DZ && m < kept) rp = p.par[m];
     };
     auto fetch_named = [&](const Unit& w) {
       n_from = n_to = 0;
@@ -812,7 +822,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e)
               if (e >= left) t[e] = 0.f;
           }
-          if (c == 0) settle();
+          if (c == 0 && __shfl_sync(0xffffffffu, owed != nullptr, 0)) settle();
+          if ((c & 1) == 0) reuse_stage();
           const uint32_t my_row = stage + lane * 128;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -831,8 +842,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) owed = dz_done + un.p;
       } else {
-        // dz of this unit has been read (by the products that this warp waited for)
-        if (warp == 2 && lane == 0) red_release(dz_used + un.p, 1u);
+        // dz of this unit has been read (by the products that this warp waited
+        // for): its buffer may be overwritten, if a later piece does
+        if (warp == 2 && lane == 0 && un.p + kDzBuffers < p.pieces) red_relaxed(dz_used + un.p, 1u);
         const bool is_dx = un.kind == DX;
         const bool last = un.p + 1 == p.pieces;  // of the vocabulary
         int splits = 1, kb_per;
@@ -846,14 +858,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int out_row = is_dx ? un.split * slot + row0 : v0 + row0;
         const int out_rows = is_dx ? kept : vn;  // rows of the job that exist
         const int row = direct && m < kept ? p.row_of[m] : 0;
-        settle();
-#pragma unroll 1
+        if (__shfl_sync(0xffffffffu, owed != nullptr, 0)) settle();
+        uint32_t vv[2][32];
+        tmem_ld32(src, vv[0]);
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tmem_ld32(src + 32 * c, v);
           const int cs = col0 + 32 * c;
           tmem_wait_ld();
-          if (c == 3) release();
+          if (c < 3) tmem_ld32(src + 32 * (c + 1), vv[(c + 1) & 1]);
+          else release();
+          uint32_t* v = vv[c & 1];
           if (un.nkb == 0) {  // no rows kept: nothing was multiplied
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = 0u;
@@ -880,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             continue;
           }
-          if (c > 1 && (f32 || (c & 1) == 0)) reuse_stage();
+          if (f32 || (c & 1) == 0) reuse_stage();
           const uint32_t my_row = stage + lane * 128;
           if (f32) {
 #pragma unroll
@@ -909,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             stage ^= 4096;
           }
         }
-        if (is_dx && lane == 0) owed = dx_done + un.p;
+        if (is_dx && !last && lane == 0) owed = dx_done + un.p;
       }
       if (more) fetch_named(nu);
       un = nu;
