@@ -52,7 +52,7 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
   p.pieces = (int)((V + cols - 1) / cols);
   p.piece = (int)(((V + p.pieces - 1) / p.pieces + kTile - 1) / kTile * kTile);
   p.pieces = (V + p.piece - 1) / p.piece;
-  p.n_ctl = kCtlPieces + 3 * p.pieces;
+  p.n_ctl = ctl_words(V, p.pieces);
   p.n_kept = take(4);
   p.ctl = take((size_t)p.n_ctl * 4);
   p.par = take((size_t)p.rows_pad * sizeof(RowPar));

@@ -26,6 +26,7 @@
 // clusters of two CTAs, each pair taking 256 x 256 output tiles (units) one
 // after the other from a common counter. The backward's units are ordered
 //     dz(0) dz(1) | dW(0) dx(0) dz(2) | dW(1) dx(1) dz(3) | ...
+// (dx before dW where its units are the longer ones)
 // with dz in three buffers, so what a unit waits for (its piece's dz, the
 // readers of the buffer it overwrites, the previous piece's sums in dx) was
 // handed out a whole group of units earlier. Waits are on counters in global
@@ -55,12 +56,16 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 96 + 32 * kEpiWarps;  // TMA, MMA, epilogue, hand-out / target warps
 constexpr int kDzBuffers = 3;
 constexpr int kTickets = 4;  // units known ahead, a ring in shared memory
+// A pair takes its next unit when the loads of the last one end in kAhead
+// stages (numbers taken earlier would keep long units from idle pairs at the
+// end: 11 % of the backward at C = 768); units shorter than that run ahead.
+constexpr int kAhead = 10;
 constexpr int kSmRing = 0;
 constexpr int kSmStage = kStages * kStageBytes;          // 2 x 4 KB per epilogue warp
 constexpr int kSmBars = kSmStage + kEpiWarps * 8192;
 constexpr int bFull = 0, bEmpty = kStages, bAccFull = 2 * kStages, bAccEmpty = 2 * kStages + 2,
-              bTkFull = 2 * kStages + 4, bTkEmpty = bTkFull + kTickets;
-constexpr int kNumBars = bTkEmpty + kTickets;
+              bTkFull = 2 * kStages + 4, bTkEmpty = bTkFull + kTickets, bWant = bTkEmpty + kTickets;
+constexpr int kNumBars = bWant + 2;  // (one to keep what follows 16-byte aligned)
 constexpr int kSmTickets = kSmBars + kNumBars * 8;       // kTickets x 32 bytes
 constexpr int kSmMisc = kSmTickets + kTickets * 32;
 constexpr int kSmAlloc = kSmMisc + 16;
@@ -106,11 +111,14 @@ struct Params {
   int row_pitch;
   const float* acc;      // fp32 sums of dx, slot_rows(kept) rows per split
   __nv_bfloat16* dx;
-  // zero at launch: [0] the next unit; then per piece finished dz, consumed dz,
-  // finished dx
+  // zero at launch: [0] the next unit; then counters, in epilogue warps: per
+  // piece readers of dz and finished dx, per 256 vocabulary columns finished dz
   unsigned* ctl;
 };
-constexpr int kCtlPieces = 4;  // first per-piece counter in ctl, three per piece
+constexpr int kCtlPieces = 4;  // first per-piece counter in ctl
+__host__ __device__ inline int ctl_words(int V, int pieces) {
+  return kCtlPieces + 2 * pieces + (V + kTile - 1) / kTile;
+}
 
 // dx has few tiles when few rows are kept: its K axis (the vocabulary) is
 // then split over units, each with an accumulator of its own that a closing
@@ -138,6 +146,7 @@ struct Sched {
   int tm, tc;          // tiles of kept rows, of C
   int kb_c, kb_n;      // K blocks of the logits, of dW
   int splits, kb_per;  // of dx over a whole piece
+  bool dx_first;       // the longer units of a group go first
   __host__ __device__ int cols(int p) const { return p + 1 < pieces ? piece : V - p * piece; }
   __host__ __device__ int tv(int p) const { return (cols(p) + kTile - 1) / kTile; }
   __host__ __device__ int kb_v(int p) const { return (cols(p) + kKB - 1) / kKB; }
@@ -158,6 +167,7 @@ __host__ __device__ inline Sched make_sched(const Params& p, int kept) {
   s.kb_c = (p.C + kKB - 1) / kKB;
   s.kb_n = (kept + kKB - 1) / kKB;
   split_dx(s.tm * s.tc, s.kb_v(0), s.splits, s.kb_per);
+  s.dx_first = s.kb_per > s.kb_n;
   return s;
 }
 
@@ -206,25 +216,30 @@ __device__ __forceinline__ Unit find_unit(const Sched& s, int u) {
   int p = s.pieces > 3 ? min(u / group, s.pieces - 3) : 0;
   u -= p * group;
   for (; p < s.pieces; ++p) {
-    if (u < s.dw(p)) {
-      o.kind = DW;
-      o.p = p;
-      o.nkb = s.kb_n;
-      band_tile(u, s.tv(p), s.tc, kBand, o.tm, o.tn);
-      return o;
+    for (int k = 0; k < 2; ++k) {
+      if ((k == 0) == s.dx_first) {
+        if (u < s.dx(p)) {
+          o.kind = DX;
+          o.p = p;
+          const int tiles = s.tm * s.tc;
+          o.split = u / tiles;
+          band_tile(u - o.split * tiles, s.tm, s.tc, kBand, o.tm, o.tn);
+          o.kb0 = o.split * s.kb_per;
+          o.nkb = min(s.kb_v(p), o.kb0 + s.kb_per) - o.kb0;
+          return o;
+        }
+        u -= s.dx(p);
+      } else {
+        if (u < s.dw(p)) {
+          o.kind = DW;
+          o.p = p;
+          o.nkb = s.kb_n;
+          band_tile(u, s.tv(p), s.tc, kBand, o.tm, o.tn);
+          return o;
+        }
+        u -= s.dw(p);
+      }
     }
-    u -= s.dw(p);
-    if (u < s.dx(p)) {
-      o.kind = DX;
-      o.p = p;
-      const int tiles = s.tm * s.tc;
-      o.split = u / tiles;
-      band_tile(u - o.split * tiles, s.tm, s.tc, kBand, o.tm, o.tn);
-      o.kb0 = o.split * s.kb_per;
-      o.nkb = min(s.kb_v(p), o.kb0 + s.kb_per) - o.kb0;
-      return o;
-    }
-    u -= s.dx(p);
     if (p + 2 < s.pieces) {
       if (u < s.dz(p + 2)) {
         logits(DZ, p + 2);
@@ -260,6 +275,14 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y,
 __device__ __forceinline__ float ld_shared_f32(uint32_t a) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_shared_v4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ void st_shared_f32(uint32_t a, float v) {
@@ -416,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // readers: the epilogue and TMA warps of both CTAs, CTA 0's MMA warp
       mbar_init(bar(bTkEmpty + t), 2 * kEpiWarps + 3);
     }
+    mbar_init(bar(bWant), 1);
     *abort_flag = 0;
     prefetch_tensor_map(&maps.x_k);
     prefetch_tensor_map(&maps.w_k);
@@ -457,9 +481,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive_read(map_rank(bar(bTkEmpty + t), 0));
     return more;
   };
-  unsigned* const dz_done = p.ctl + kCtlPieces;
-  unsigned* const dz_used = dz_done + p.pieces;
+  unsigned* const dz_used = p.ctl + kCtlPieces;
   unsigned* const dx_done = dz_used + p.pieces;
+  unsigned* const dz_done = dx_done + p.pieces;  // by vocabulary tile
 
   // The TMA and MMA warps run their loops converged, one elected lane issuing:
   // the operands of the issue then live in uniform registers. Issued from a
@@ -471,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool all = kept == p.N;  // every row kept: x is read in place
     int s = 0;
     uint32_t phase = 1;  // a fresh barrier's previous phase counts as complete
-    int dz_ok = -1, used_ok = -1, dx_ok = -1;  // pieces whose counters are known to be full
+    int used_ok = -1, dx_ok = -1;  // pieces whose counters are known to be full
     bool ok = true;
     Unit un;
     for (int n = 0; ok && next_unit(n, un); ++n) {
@@ -500,10 +524,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           mb = all ? &maps.x_mn : &maps.xc_mn;
           a_mn = true;
         }
-        if (un.p > dz_ok) {
-          if (!warp_count(dz_done + un.p, 2u * kEpiWarps * sc.dz(un.p), abort_flag)) break;
-          dz_ok = un.p;
-        }
+        // dz of its vocabulary tiles, a lane per tile: of one (dW), or of its K range
+        const int t0 = un.kind == DW ? un.tm : un.kb0 / 4;
+        const int t1 = un.kind == DW ? un.tm : (un.kb0 + un.nkb - 1) / 4;
+        const unsigned want = 2u * kEpiWarps * sc.tm;
+        for (int t = t0 + lane; ok && __any_sync(0xffffffffu, t <= t1); t += 32)
+          ok = warp_count(dz_done + v0 / kTile + min(t, t1), want, abort_flag);
+        if (!ok) break;
         if (un.kind == DX && un.p - 1 > dx_ok) {
           if (!warp_count(dx_done + un.p - 1, 2u * kEpiWarps * sc.dx(un.p - 1), abort_flag)) break;
           dx_ok = un.p - 1;
@@ -515,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         if (el) {
+          if (kBwd && rank == 0 && kb == un.nkb - 1 - kAhead) mbar_arrive(bar(bWant));
           // CTA 0's barrier counts the bytes of both CTAs' boxes
           if (rank == 0) mbar_arrive_expect_tx(bar(bFull + s), 2 * kStageBytes);
           const uint32_t full = map_rank(bar(bFull + s), 0);
@@ -584,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- hand-out of units to both CTAs ----------------
     // A warp of its own: taking a number and finding its unit are long chains
     // that would hold up the loads.
+    int wants = 0;
     for (int n = 0; kBwd; ++n) {
       const int t = n % kTickets;
       if (!warp_wait_cl(bar(bTkEmpty + t), ((n / kTickets) & 1) ^ 1, abort_flag)) break;
@@ -598,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (un.kind == END) break;
+      if (un.nkb > kAhead && !warp_wait(bar(bWant), wants++ & 1, abort_flag)) break;
     }
   } else if (warp == 2 + kEpiWarps) {
     // ---------------- the target's logit ----------------
@@ -840,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             stage ^= 4096;
           }
         }
-        if (lane == 0) owed = dz_done + un.p;
+        if (lane == 0) owed = dz_done + v0 / kTile + un.tn;
       } else {
         // dz of this unit has been read (by the products that this warp waited
         // for): its buffer may be overwritten, if a later piece does
@@ -874,24 +904,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (cs >= p.C || row0 >= out_rows) continue;  // uniform in the warp
           if (direct) {
-            if (m < kept) {
-              const float4* before = reinterpret_cast<const float4*>(p.acc + (size_t)m * p.C + cs);
-              uint4* out = reinterpret_cast<uint4*>(p.dx + (size_t)row * p.C + cs);
+            // by way of the staging, so that eight lanes read and write a row:
+            // a row per lane took 20 us at the end of the call
+            float4 sum[8];
+            const int quad = lane & 7, cq = cs + 4 * quad;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (cs + 8 * e >= p.C) break;  // C % 8 == 0
-                float f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * e + i]);
-                if (un.p > 0) {
-                  const float4 x = __ldcg(before + 2 * e), y = __ldcg(before + 2 * e + 1);
-                  f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-                  f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
-                }
-                out[e] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                    pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-              }
+            for (int i = 0; i < 8; ++i) {
+              const int r = 4 * i + (lane >> 3);
+              sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (un.p > 0 && row0 + r < kept && cq < p.C)
+                sum[i] = __ldcg(reinterpret_cast<const float4*>(p.acc + (size_t)(row0 + r) * p.C + cq));
             }
+            reuse_stage();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              st_shared_v4(stage + lane * 128 + ((e ^ sw) << 4), v[4 * e], v[4 * e + 1],
+                           v[4 * e + 2], v[4 * e + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = 4 * i + (lane >> 3);
+              const int to = __shfl_sync(0xffffffffu, row, r);
+              const float4 f = ld_shared_v4(stage + r * 128 + ((quad ^ (r & 7)) << 4));
+              if (row0 + r < kept && cq < p.C)
+                *reinterpret_cast<uint2*>(p.dx + (size_t)to * p.C + cq) =
+                    make_uint2(pack_bf16(sum[i].x + f.x, sum[i].y + f.y),
+                               pack_bf16(sum[i].z + f.z, sum[i].w + f.w));
+            }
+            __syncwarp();
             continue;
           }
           if (f32 || (c & 1) == 0) reuse_stage();
