@@ -29,9 +29,9 @@ bool head_sizes_ok(int N, int V, int C, int K) {
   if (N <= 0 || V <= 0 || C <= 0 || K < 0 || K > head100::kMaxNamed) return false;
   if (C % 8 != 0 || C > (1 << 20) || N > (1 << 26) || V > (1 << 26)) return false;
   const long tiles_n = N / 256 + 1, tiles_v = V / 256 + 1, tiles_c = C / 256 + 1;
-  // units of one launch: the largest pieces of all three products
+  // the units of a call are numbered in 32 bits: dz, dW, and dx per piece
   return tiles_n * tiles_v < (1L << 28) && tiles_v * tiles_c < (1L << 28) &&
-         tiles_n * tiles_c < (1L << 22);
+         tiles_n * tiles_c * (V / kDzMinCols + 1) < (1L << 28);
 }
 
 // K = 0: a single target per row (attn_head_ce), else teacher entries per row.

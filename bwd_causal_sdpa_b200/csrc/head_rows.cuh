@@ -110,17 +110,21 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowsArgs a
   }
   if (total == a.N) return;  // the products read x in place
   // a warp copies a row at a time (its pos entries were written by this block)
+  const uint4* __restrict__ x = a.x;
+  uint4* __restrict__ xc = a.xc;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
   for (int r = r0 + warp; r < r1; r += kWarps) {
     const int at = a.pos[r];
     if (at >= 0) {
-      for (int i = lane; i < a.c8; i += 32) a.xc[(size_t)at * a.c8 + i] = a.x[(size_t)r * a.c8 + i];
+#pragma unroll 4
+      for (int i = lane; i < a.c8; i += 32) xc[(size_t)at * a.c8 + i] = x[(size_t)r * a.c8 + i];
     } else if (a.dx) {
-      for (int i = lane; i < a.c8; i += 32) a.dx[(size_t)r * a.c8 + i] = make_uint4(0, 0, 0, 0);
+      for (int i = lane; i < a.c8; i += 32) a.dx[(size_t)r * a.c8 + i] = zero;
     }
   }
   const int pad = slot_rows(total);
   for (int r = total + blockIdx.x * kWarps + warp; r < pad; r += gridDim.x * kWarps)
-    for (int i = lane; i < a.c8; i += 32) a.xc[(size_t)r * a.c8 + i] = make_uint4(0, 0, 0, 0);
+    for (int i = lane; i < a.c8; i += 32) xc[(size_t)r * a.c8 + i] = zero;
 }
 
 // The teacher's list of one row per warp: q = softmax of t / tau over the

@@ -370,7 +370,8 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
  * included) reaches nothing. The backward also leaves out a row whose dloss
  * and dlse are both 0. The products cost what the rows that are kept cost;
  * with none kept dx and dw are 0. A target or id >= V is treated as absent
- * and the status word reports ATTN_EDEVICE_INPUT. Every output is overwritten.
+ * and the status word reports ATTN_EDEVICE_INPUT. Every output is overwritten,
+ * and none may overlap an input or the workspace.
  *
  * lse given to the backward is what the forward wrote for the same x, w and
  * temperature. dz is rounded once to bf16, the tensor cores' operand type
@@ -385,8 +386,10 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
  *
  * Workspace: attn_head_workspace_bytes(N, V, C, K, is_bwd) bytes, K = 0 for
  * attn_head_ce*; 0 for invalid sizes. The backward takes the vocabulary in
- * pieces, so its workspace does not grow with V: about 3 x 96 MiB for dz (up
- * to 24576 rows) plus the fp32 sums of dx. Pure host function.
+ * pieces, so its workspace does not grow with V: at most 3 x 96 MiB for dz up
+ * to 24576 rows (3 x 4096 bytes a row beyond), plus the kept rows of x and the
+ * fp32 sums of dx. (A teacher's lists add N (8 K + V / 64) bytes.) Pure host
+ * function.
  */
 size_t attn_head_workspace_bytes(int N, int V, int C, int K, int is_bwd);
 int attn_head_ce(const void* x, const void* w, const int32_t* target, float* loss, float* lse,

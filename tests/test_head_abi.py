@@ -90,11 +90,17 @@ def test_workspace_bytes():
             assert ws(*bad, b) == 0
     # the forward keeps 8 bytes per 128 logits, never the logits
     assert ws(8192, 32063, 2048, 0, 0) < 8192 * 32063 * 2 // 8
-    # the backward's does not grow with the vocabulary
-    a, b = (ws(8192, v, 2048, 0, 1) for v in (32063, 1 << 22))
-    assert b <= a + (1 << 20) and a < 8192 * 32063 * 2
+    # the backward's does not grow with the vocabulary: three pieces of dz of at
+    # most 96 MiB, the kept rows of x (bf16), the sums of dx (fp32), and small
+    # arrays by row and by 256 vocabulary rows
+    for v in (32063, 50000, 1 << 20, 1 << 22):
+        got = ws(8192, v, 2048, 0, 1)
+        assert got <= 3 * (96 << 20) + 8192 * 2048 * (2 + 4) + (1 << 20), v
+    assert ws(8192, 32063, 2048, 0, 1) < 8192 * 32063 * 2
     # one buffer of dz where one piece holds the vocabulary
     assert ws(256, 1000, 64, 0, 1) % 256 == 0
+    # units are numbered in 32 bits
+    assert ws(1 << 26, 1 << 26, 64, 0, 1) == 0
     assert _ce(ws_bytes=ws(10, 100, 64, 0, 0) - 1) == A.ATTN_EWORKSPACE
     assert _ce_bwd(ws_bytes=ws(10, 100, 64, 0, 1) - 1) == A.ATTN_EWORKSPACE
     assert _distill(ws_bytes=ws(10, 100, 64, 4, 0) - 1) == A.ATTN_EWORKSPACE

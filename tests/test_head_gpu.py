@@ -351,3 +351,84 @@ def test_output_projection_feeds_the_loss():
     errs = {"loss": rel_fro(f(loss), rl), "dw": rel_fro(f(dw), rdw), "d_o": rel_fro(f(d_o), rdo),
             "dw_o": rel_fro(f(dw_o), rdwo)}
     assert all(e <= 1e-2 for e in errs.values()), errs
+
+
+@pytest.mark.parametrize("N,K", [(200, 1024), (256, 40), (1, 40)])
+def test_one_row_tile_with_a_teacher(N, K):
+    """The forward that takes all rows as they are: rows left out among them
+    hold NaN, ids repeat and crowd."""
+    w = make_head_workload(head_config_by_name("head_distill_small"), N=N, K=K, V=1500, C=64,
+                           left_out=0.3, seed=90 + N)
+    out = (w.t_idx < 0).all(axis=1)
+    w.x[out] = np.nan
+    _check(w)
+
+
+@pytest.mark.parametrize("name", ["head_small", "head_distill_small"])
+@pytest.mark.parametrize("N,V,C", [(70, 900, 96), (513, 4100, 640), (1030, 2000, 1544)])
+def test_workspace_of_the_stated_size_is_enough(name, N, V, C):
+    """The stated bytes and no more: what follows the workspace stays, and what
+    it held before does not matter."""
+    import torch
+
+    import bwd_causal_sdpa_b200 as A
+    from bwd_causal_sdpa_b200.runner import HeadRunner
+
+    w = make_head_workload(head_config_by_name(name), N=N, V=V, C=C)
+    K = w.cfg.K
+    ref, _ = _check(w)
+    for fill in (0x00, 0xFF):
+        r = HeadRunner(w)
+        for is_bwd, call in ((0, r.forward), (1, r.backward)):
+            nb = A.attn_head_workspace_bytes(N, V, C, K, is_bwd)
+            buf = torch.full((nb + 4096,), fill, dtype=torch.uint8, device="cuda")
+            buf[nb:] = 0x5A
+            r.ws, r.ws_bytes = buf, nb
+            call()
+            torch.cuda.synchronize()
+            assert (buf[nb:] == 0x5A).all()
+        for n in ("loss", "lse", "dx", "dw"):
+            assert torch.equal(getattr(r, n), getattr(ref, n)), n
+
+
+@pytest.mark.parametrize("name,left_out", [("head_237m", 0.0), ("head_237m", 0.93),
+                                           ("head_8k", 0.3), ("head_distill_8k", 0.1)])
+def test_full_size_against_64_bits(name, left_out):
+    """The training shapes, against plain float64 products on the device.
+    Relative Frobenius bounds: dx and dW carry two independent roundings to
+    bf16 of rms at most 2^-8 / sqrt(3) each: 2^-8 sqrt(2 / 3) = 3.2e-3 < 4e-3;
+    loss and lse the fp32 sums of their logits (2e-6, two to three digits
+    above 2^-23)."""
+    import torch
+
+    from bwd_causal_sdpa_b200 import ATTN_OK
+    from bwd_causal_sdpa_b200.runner import HeadRunner
+
+    w = make_head_workload(head_config_by_name(name), left_out=left_out)
+    c = w.cfg
+    r = HeadRunner(w)
+    r.forward()
+    r.backward()
+    assert r.status() == ATTN_OK
+    ids, q = _lists(w)
+    ids, q = torch.from_numpy(ids).cuda(), torch.from_numpy(q).cuda()
+    x, W = r.x.double(), r.wt.double()
+    kept = (ids >= 0).any(dim=1)
+    loss, lse = (torch.zeros(c.N, dtype=torch.float64, device="cuda") for _ in range(2))
+    dx, dw = torch.zeros_like(x), torch.zeros_like(W)
+    for i in range(0, c.N, 1024):
+        s = slice(i, i + 1024)
+        z = x[s] @ W.T / c.tau
+        l = torch.logsumexp(z, dim=1)
+        at = z.gather(1, ids[s].clamp(min=0))
+        terms = torch.where(q[s] > 0, q[s] * (torch.log(q[s].clamp(min=1e-300)) - at + l[:, None]), 0.0)
+        loss[s], lse[s] = terms.sum(dim=1) * kept[s], l * kept[s]
+        g = r.dloss[s].double() * kept[s]
+        dz = torch.exp(z - l[:, None]) * (g + r.dlse[s].double() * kept[s])[:, None]
+        dz.scatter_add_(1, ids[s].clamp(min=0), -g[:, None] * q[s])
+        dz = dz / c.tau
+        dx[s] = dz @ W
+        dw += dz.T @ x[s]
+    for n, ref, tol in (("loss", loss, 2e-6), ("lse", lse, 2e-6), ("dx", dx, 4e-3), ("dw", dw, 4e-3)):
+        err = ((getattr(r, n).double() - ref).norm() / ref.norm()).item()
+        assert err <= tol, (n, err)
