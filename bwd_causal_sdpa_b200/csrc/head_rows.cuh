@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
 constexpr int kLossThreads = 128;
 __global__ void __launch_bounds__(kLossThreads)
     head_loss_kernel(const float2* __restrict__ part, const float* __restrict__ named,
+                     const float* __restrict__ exact, const int* __restrict__ ids,
                      const float* __restrict__ share, const float* __restrict__ entropy,
                      const int* __restrict__ pos, const int* __restrict__ target,
                      const int* __restrict__ flags, float* __restrict__ loss,
@@ -271,12 +272,29 @@ __global__ void __launch_bounds__(kLossThreads)
             : s + os;
     m = nm;
   }
-  const float l = (m + log2f(s)) * kLn2;
+  float l = (m + log2f(s)) * kLn2;
   float d = 0.f;
+  const size_t own = (size_t)(at >= 0 ? at : 0) * K;
+  const float* z = named;
+  if (exact) {
+    // lse takes the named logits' more exact values too: each moves it by its
+    // share of the softmax times the difference (an id named twice, once)
+    z = exact;
+    if (at >= 0)
+      for (int k = slice; k < K; k += 8) {
+        const int id = ids[(size_t)r * K + k];
+        const bool again = k > 0 && ids[(size_t)r * K + k - 1] == id;
+        const float diff = exact[own + k] - named[own + k];
+        if ((unsigned)id < (unsigned)V && !again && diff != 0.f) d += expf(named[own + k] - l) * diff;
+      }
+    for (int o = 4; o < 32; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    l += d;
+    d = 0.f;
+  }
   if (at >= 0)
     for (int k = slice; k < K; k += 8) {
       const float q = share ? share[(size_t)r * K + k] : 1.f;
-      if (q != 0.f) d += q * (l - named[(size_t)at * K + k]);
+      if (q != 0.f) d += q * (l - z[own + k]);
     }
   for (int o = 4; o < 32; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
   if (slice == 0 && r < N) {

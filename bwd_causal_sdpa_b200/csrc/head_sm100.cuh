@@ -53,7 +53,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kPairs = 74;            // CTA pairs of a full persistent grid (148 SMs)
 
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 96 + 32 * kEpiWarps;  // TMA, MMA, epilogue, hand-out / target warps
+constexpr int kThreads = 96 + 32 * kEpiWarps;  // TMA, MMA, epilogue, hand-out or dot-product warps
 constexpr int kDzBuffers = 3;
 constexpr int kTickets = 4;  // units known ahead, a ring in shared memory
 // A pair takes its next unit when the loads of the last one end in kAhead
@@ -108,6 +108,7 @@ struct Params {
   int first_pitch;
   float2* part;          // LSE: [2 tiles][row_pitch] maximum (base 2), sum
   float* named;          // LSE: [kept row][K] z at the row's ids
+  float* exact;          // the same from plain fp32 sums, for few ids per row, or null
   int row_pitch;
   const float* acc;      // fp32 sums of dx, slot_rows(kept) rows per split
   __nv_bfloat16* dx;
@@ -630,31 +631,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (un.nkb > kAhead && !warp_wait(bar(bWant), wants++ & 1, abort_flag)) break;
     }
   } else if (warp == 2 + kEpiWarps) {
-    // ---------------- the target's logit ----------------
-    // A single named id per row is a dot product of its own, in plain fp32: the
-    // loss is the difference lse - z, and the tensor core's sums, cut instead
-    // of rounded, would leave about 1e-6 of it. Runs beside the products.
-    if (!kBwd && !p.share) {
-      const int c8 = p.C / 8;
-      for (int m = blockIdx.x >> 1; m < kept; m += gridDim.x >> 1) {
-        const int row = p.n_kept ? p.row_of[m] : m;
-        const int id = p.ids[row];
-        if ((unsigned)id >= (unsigned)p.V) continue;
-        const uint4* xr = p.x + (size_t)row * c8;
-        const uint4* wr = p.w + (size_t)id * c8;
+    // ---------------- the named logits ----------------
+    // With few named ids per row their logits are also taken as dot products in
+    // plain fp32, four at a time, eight lanes each, beside the products: the
+    // loss is a difference of logits, and the tensor core's sums, cut instead
+    // of rounded, would leave 1e-6 to 3e-6 of it.
+    if (!kBwd && p.exact) {
+      const int c8 = p.C / 8, sub = lane & 7;
+      const long items = (long)kept * p.K;
+      for (long i0 = (long)(blockIdx.x >> 1) * 4; i0 < items; i0 += (long)(gridDim.x >> 1) * 4) {
+        const long i = i0 + (lane >> 3);
+        const int m = (int)(i / p.K);
+        int row = 0, id = -1;
+        if (i < items) {
+          row = p.n_kept ? p.row_of[m] : m;
+          id = p.ids[(size_t)row * p.K + (int)(i - (long)m * p.K)];
+        }
         float s0 = 0.f, s1 = 0.f;
+        if ((unsigned)id < (unsigned)p.V) {
+          const uint4* xr = p.x + (size_t)row * c8;
+          const uint4* wr = p.w + (size_t)id * c8;
 #pragma unroll 4
-        for (int i = lane; i < c8; i += 32) {
-          const uint4 a = xr[i], b = wr[i];
-          const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+          for (int q = sub; q < c8; q += 8) {
+            const uint4 a = xr[q], b = wr[q];
+            const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s0 = fmaf(__uint_as_float(av[e] << 16), __uint_as_float(bv[e] << 16), s0);
-            s1 = fmaf(__uint_as_float(av[e] & 0xffff0000u), __uint_as_float(bv[e] & 0xffff0000u), s1);
+            for (int e = 0; e < 4; ++e) {
+              s0 = fmaf(__uint_as_float(av[e] << 16), __uint_as_float(bv[e] << 16), s0);
+              s1 = fmaf(__uint_as_float(av[e] & 0xffff0000u), __uint_as_float(bv[e] & 0xffff0000u),
+                        s1);
+            }
           }
         }
-        s0 = warp_sum(s0 + s1);
-        if (lane == 0) p.named[m] = s0 * p.inv_tau;
+        s0 += s1;
+        for (int o = 1; o < 8; o <<= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+        if (sub == 0 && i < items) p.exact[i] = s0 * p.inv_tau;
       }
     }
   } else {
@@ -689,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n_from = 0, n_to = 0;
     auto fetch_row = [&](const Unit& w) {
       const int m = w.tm * kTile + rank * 128 + sub * 32 + lane;
-      if (!kBwd && !p.n_kept) rp.id = m;
+      if (!kBwd && !p.n_kept) rp.id = m < kept && !p.share ? p.ids[m] : m;
       else if (w.kind <= DZ && m < kept) rp = p.par[m];
     };
     auto fetch_named = [&](const Unit& w) {
@@ -721,7 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         share = p.share + (size_t)rp.id * p.K;
       }
       const float lse2 = rp.lse2, ca = rp.ca, cb = rp.cb;
-      const int target = rp.id - (v0 + col0);  // without a list: within these columns or not
+      // without a list: within these columns or not
+      const int target = m < kept ? rp.id - (v0 + col0) : -1;
       const uint32_t full = bar(bAccFull + a), par = (n >> 1) & 1;
       if (!__all_sync(0xffffffffu, mbar_test(full, par))) settle();  // others may wait for it: never block owing
       if (!warp_wait(full, par, abort_flag)) break;
@@ -762,6 +774,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               nm.advance();
             }
             __syncwarp();
+          }
+          if (!p.share && __any_sync(0xffffffffu, (unsigned)(target - 32 * c) < 32u)) {
+            float z = 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (target == 32 * c + e) z = __uint_as_float(t[e]);
+            if ((unsigned)(target - 32 * c) < 32u) p.named[m] = z * p.inv_tau;
           }
           float f[32];
 #pragma unroll
