@@ -123,12 +123,12 @@ __host__ __device__ inline int ctl_words(int V, int pieces) {
 
 // dx has few tiles when few rows are kept: its K axis (the vocabulary) is
 // then split over units, each with an accumulator of its own that a closing
-// pass adds in order (no atomics on values: results repeat). One unit per CTA
-// pair, at least eight K blocks each.
+// pass adds in order (no atomics on values: results repeat). At most one unit
+// per CTA pair, at least eight K blocks each.
 __host__ __device__ inline void split_dx(int tiles, int kb_total, int& splits, int& kb_per) {
   splits = 1;
   if (tiles > 0 && tiles < kPairs) {
-    splits = (kPairs + tiles - 1) / tiles;
+    splits = kPairs / tiles;
     const int most = kb_total / 8 > 1 ? kb_total / 8 : 1;
     splits = splits < most ? splits : most;
   }
@@ -168,7 +168,9 @@ __host__ __device__ inline Sched make_sched(const Params& p, int kept) {
   s.kb_c = (p.C + kKB - 1) / kKB;
   s.kb_n = (kept + kKB - 1) / kKB;
   split_dx(s.tm * s.tc, s.kb_v(0), s.splits, s.kb_per);
-  s.dx_first = s.kb_per > s.kb_n;
+  // split dx units are one per pair and the last to have their dz: they end a
+  // group (100 rows, first: 54 us)
+  s.dx_first = s.splits == 1 && s.kb_per > s.kb_n;
   return s;
 }
 
@@ -371,6 +373,37 @@ __device__ __forceinline__ bool warp_count(const unsigned* c, unsigned want,
   return __all_sync(0xffffffffu, wait_count(c, want, abort_flag));
 }
 
+// Bounded wait for the counters of tiles t0 to t1, a lane per tile; also looks
+// at those behind (up to `end`): `to` is one past the last of the tiles from t0
+// on that were there without a gap.
+__device__ __forceinline__ bool wait_tiles(const unsigned* done, int t0, int t1, int end,
+                                           unsigned want, int lane, int& to,
+                                           volatile int* abort_flag) {
+  const long long start = clock64();
+  bool ok = true;
+  to = t0;
+  while (to <= t1) {
+    const int t = to + lane;
+    const bool there = t < end && ld_acquire(done + t) >= want;
+    const unsigned gap = ~__ballot_sync(0xffffffffu, there);
+    to += gap ? __ffs(gap) - 1 : 32;
+    if (to <= t1 && (gap & 1u)) {
+      ok = *abort_flag == 0;
+      if (ok && clock64() - start > kWaitLimitCycles) {
+        *abort_flag = 1;
+        report_status(ATTN_ETIMEOUT);
+        ok = false;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      __nanosleep(100);
+    }
+  }
+  __syncwarp();
+  fence_proxy_async();
+  return ok;
+}
+
 // 128 rows (K contiguous: row0.., K from k0) or 128 columns (row index
 // contiguous: from row0, 64 K rows from k0) of an operand into dst.
 __device__ __forceinline__ void load_operand(const CUtensorMap* m, bool mn, bool one_box, int row0,
@@ -497,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0;
     uint32_t phase = 1;  // a fresh barrier's previous phase counts as complete
     int used_ok = -1, dx_ok = -1;  // pieces whose counters are known to be full
+    int dz_from = 0, dz_to = 0;    // vocabulary tiles whose dz is known to be there
     bool ok = true;
     Unit un;
     for (int n = 0; ok && next_unit(n, un); ++n) {
@@ -525,13 +559,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           mb = all ? &maps.x_mn : &maps.xc_mn;
           a_mn = true;
         }
-        // dz of its vocabulary tiles, a lane per tile: of one (dW), or of its K range
-        const int t0 = un.kind == DW ? un.tm : un.kb0 / 4;
-        const int t1 = un.kind == DW ? un.tm : (un.kb0 + un.nkb - 1) / 4;
-        const unsigned want = 2u * kEpiWarps * sc.tm;
-        for (int t = t0 + lane; ok && __any_sync(0xffffffffu, t <= t1); t += 32)
-          ok = warp_count(dz_done + v0 / kTile + min(t, t1), want, abort_flag);
-        if (!ok) break;
+        // dz of its vocabulary tiles: of one (dW), or of its K range
+        const int t0 = v0 / kTile + (un.kind == DW ? un.tm : un.kb0 / 4);
+        const int t1 = v0 / kTile + (un.kind == DW ? un.tm : (un.kb0 + un.nkb - 1) / 4);
+        if (t0 < dz_from || t1 >= dz_to) {
+          ok = wait_tiles(dz_done, t0, t1, v0 / kTile + sc.tv(un.p), 2u * kEpiWarps * sc.tm, lane,
+                          dz_to, abort_flag);
+          dz_from = t0;
+          if (!ok) break;
+        }
         if (un.kind == DX && un.p - 1 > dx_ok) {
           if (!warp_count(dx_done + un.p - 1, 2u * kEpiWarps * sc.dx(un.p - 1), abort_flag)) break;
           dx_ok = un.p - 1;
