@@ -12,6 +12,7 @@ namespace {
 // Vocabulary rows per piece of the backward: the dz buffer of a piece (three
 // are in use) takes up to 96 MiB, or 2048 columns when the rows are many
 // (shorter pieces would add into dx more often than their products are worth).
+// 8192 rows of width 2048: 2.61 ms with 64 MiB, 2.55 with 96, 2.56 with 160.
 constexpr size_t kDzBytes = (size_t)96 << 20;
 constexpr long kDzMinCols = 2048;
 
@@ -115,8 +116,8 @@ bool head_map(CUtensorMap* m, const void* base, bool f32, long rows, long cols, 
 }
 
 // The same matrix in 64-column blocks, two of them (64 rows each) per box:
-// [cols / 64][rows][64]. A box of 128 rows of 128 bytes moves faster than two
-// of 64. cols % 64 == 0.
+// [cols / 64][rows][64]. One box of 128 rows of 128 bytes moves 83 bytes per
+// cycle and SM, boxes of 64 rows 66. cols % 64 == 0.
 bool head_block_map(CUtensorMap* m, const void* base, long rows, long cols) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;

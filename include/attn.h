@@ -342,7 +342,8 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
  * log-sum-exp and its LM head; Forge README, "Architecture", the
  * cross-entropy kernels). The logits are formed tile by tile on the tensor
  * cores (bf16 operands, fp32 accumulation) and never written; lse, softmax
- * statistics, losses and dx sums are fp32.
+ * statistics, losses and dx sums are fp32. With up to four entries per row
+ * their logits are taken in plain fp32 besides.
  *
  *   attn_head_ce:      q = 1 at target[n] (tau = 1):
  *                      loss[n] = lse[n] - z[n][target[n]]
@@ -375,7 +376,7 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
  *
  * lse given to the backward is what the forward wrote for the same x, w and
  * temperature. dz is rounded once to bf16, the tensor cores' operand type
- * (2^-9 relative at most), before its two products: dw carries that rounding
+ * (2^-8 relative at most, half a step), before its two products: dw carries that rounding
  * in either type. Results do not depend on atomics: the same call gives the
  * same bits.
  *
