@@ -16,16 +16,11 @@ namespace {
 constexpr size_t kDzBytes = (size_t)96 << 20;
 constexpr long kDzMinCols = 2048;
 
-// Named ids per row up to which the forward also takes their logits in plain
-// fp32. More of them average the errors that this is about, and their rows of
-// W would cost more than the products hide.
-constexpr int kExactNamed = 4;
-
 struct HeadPlan {
   int rows_pad = 0, piece = 0, pieces = 0, parts = 0;
   size_t n_kept = 0, ctl = 0, row_of = 0, pos = 0, par = 0, xc = 0, ids = 0, share = 0, entropy = 0, flags = 0, first = 0;
   size_t part = 0, named = 0, exact = 0;  // forward
-  size_t dz[head100::kDzBuffers] = {}, acc = 0;  // backward
+  size_t dz[head100::kDzBuffers] = {}, acc = 0, rest = 0;  // backward
   long acc_rows = 0;
   int n_ctl = 0, first_pitch = 0;
   size_t total = 0;
@@ -77,7 +72,7 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
     p.parts = 2 * ((V + kTile - 1) / kTile);
     p.part = take((size_t)p.parts * p.rows_pad * sizeof(float2));
     p.named = take((size_t)N * std::max(K, 1) * 4);
-    if (K <= kExactNamed) p.exact = take((size_t)N * std::max(K, 1) * 4);
+    if (K <= kFewNamed) p.exact = take((size_t)N * std::max(K, 1) * 4);
     p.total = off;
     return p;
   }
@@ -93,6 +88,7 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
   }
   p.acc_rows = rows;
   p.acc = take((size_t)rows * C * 4);
+  if (K <= kFewNamed) p.rest = take((size_t)N * std::max(K, 1) * 4);
   p.total = off;
   return p;
 }
@@ -173,8 +169,8 @@ int head_gemm(const head100::Maps& maps, const head100::Params& p, cudaStream_t 
   // pairs beyond the units that any number of kept rows gives would be idle
   const Sched s = make_sched(p, p.N);
   long units = kBwd ? kPairs : s.dz(0);
-  // the fp32 logits of few named ids want warps, four of them each
-  if (!kBwd && p.exact) units = std::max(units, ((long)p.N * p.K + 3) / 4);
+  // the fp32 logits of few named ids want warps, four of them each (two a pair)
+  if (!kBwd && p.exact) units = std::max(units, ((long)p.N * p.K + 7) / 8);
   const unsigned pairs = (unsigned)std::min<long>(units, kPairs);
   ATTN_LAUNCH(KK_HEAD_GEMM, st, pdl_cluster_launch(head_gemm_kernel<kBwd>, dim3(2 * pairs), kThreads,
                                                    kSmAlloc, st, 2u, maps, p));
@@ -266,7 +262,7 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   if (!c.bwd) {
     p.part = (float2*)(ws + hp.part);
     p.named = (float*)(ws + hp.named);
-    p.exact = K <= kExactNamed ? (float*)(ws + hp.exact) : nullptr;
+    p.exact = K <= kFewNamed ? (float*)(ws + hp.exact) : nullptr;
     if (int rc = head_gemm<false>(maps, p, st)) return rc;
     ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_loss_kernel, (unsigned)((N + kLossThreads / 8 - 1) / (kLossThreads / 8)),
                                              kLossThreads, 0, st, p.part, p.named, p.exact, p.ids, share, entropy,
@@ -276,6 +272,7 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   }
 
   p.acc = (const float*)(ws + hp.acc);
+  p.rest = K <= kFewNamed ? (float*)(ws + hp.rest) : nullptr;
   p.dx = (__nv_bfloat16*)c.dx;
   p.dw_f32 = c.dw_dtype == ATTN_F32;
   p.c_blocks = C % 64 == 0;
@@ -298,8 +295,8 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   if (int rc = head_gemm<true>(maps, p, st)) return rc;
   const long n8 = (long)N * (C / 8);
   ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_dx_kernel, (unsigned)std::min<long>((n8 + 255) / 256, 148L * 8),
-                                           256, 0, st, p.acc, row_of, n_kept, (uint4*)c.dx, C,
-                                           (std::min(hp.piece, V) + kKB - 1) / kKB));
+                                           256, 0, st, p.acc, row_of, n_kept, p.rest, p.ids, p.w, (uint4*)c.dx,
+                                           V, C, p.K, (std::min(hp.piece, V) + kKB - 1) / kKB));
   return launch_status();
 }
 

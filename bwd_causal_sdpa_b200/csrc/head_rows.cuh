@@ -304,11 +304,14 @@ __global__ void __launch_bounds__(kLossThreads)
 }
 
 // dx of the kept rows where its vocabulary axis was split: the accumulators
-// added in order and rounded once. Eight columns per thread. Without a split
+// added in order, then what the rounding of dz took from the named columns, and
+// rounded once. Eight columns per thread. Without a split
 // the last piece's epilogue has written dx, and this pass ends at once.
 __global__ void __launch_bounds__(256)
     head_dx_kernel(const float* __restrict__ acc, const int* __restrict__ row_of,
-                   const int* __restrict__ n_kept, uint4* __restrict__ dx, int C, int kb_total) {
+                   const int* __restrict__ n_kept, const float* __restrict__ rest,
+                   const int* __restrict__ ids, const uint4* __restrict__ w,
+                   uint4* __restrict__ dx, int V, int C, int K, int kb_total) {
   pdl_wait_and_trigger();
   const int kept = *n_kept;
   int splits, kb_per;
@@ -320,17 +323,38 @@ __global__ void __launch_bounds__(256)
   for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256) {
     const int m = (int)(i / c8), c = (int)(i - (long)m * c8) * 8;
     const float* src = acc + (size_t)m * C + c;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+    const int row = row_of[m];
+    float g[kFewNamed];
+    uint4 wv[kFewNamed];
+#pragma unroll
+    for (int k = 0; k < kFewNamed; ++k) {
+      g[k] = 0.f;
+      wv[k] = make_uint4(0, 0, 0, 0);
+      if (rest && k < K) {
+        const int id = ids[(size_t)row * K + k];
+        if ((unsigned)id < (unsigned)V) {
+          g[k] = rest[(size_t)m * K + k];
+          wv[k] = w[(size_t)id * c8 + c / 8];
+        }
+      }
+    }
+    float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+#pragma unroll 8
     for (int s = 0; s < splits; ++s, src += slot) {
       const float4 a = *reinterpret_cast<const float4*>(src);
       const float4 b = *reinterpret_cast<const float4*>(src + 4);
-      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+      lo.x += a.x; lo.y += a.y; lo.z += a.z; lo.w += a.w;
+      hi.x += b.x; hi.y += b.y; hi.z += b.z; hi.w += b.w;
     }
-    dx[(size_t)row_of[m] * c8 + c / 8] =
-        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                   pack_bf16(v[6], v[7]));
+#pragma unroll
+    for (int k = 0; k < kFewNamed; ++k)
+      if (g[k] != 0.f) {
+        add_scaled4(lo, g[k], make_uint2(wv[k].x, wv[k].y));
+        add_scaled4(hi, g[k], make_uint2(wv[k].z, wv[k].w));
+      }
+    dx[(size_t)row * c8 + c / 8] =
+        make_uint4(pack_bf16(lo.x, lo.y), pack_bf16(lo.z, lo.w), pack_bf16(hi.x, hi.y),
+                   pack_bf16(hi.z, hi.w));
   }
 }
 

@@ -16,7 +16,9 @@
 // dz of the piece is rounded to bf16 (the tensor cores' operand type; at most
 // half a step, 2^-8 relative, which the sums of both products average) into a
 // buffer that the two products of the piece read. dx is summed over the pieces
-// in fp32, dW of a piece is final.
+// in fp32, dW of a piece is final. In a row of dx one entry of dz, the target's,
+// outweighs the others: where few ids are named, what their rounding takes is
+// kept and added to dx in fp32, times their rows of W.
 //
 // Rows whose target is absent (or whose upstream gradients are both zero) are
 // left out: the kept rows are compacted first, so the products cost what the
@@ -59,6 +61,11 @@ constexpr int kOperandBytes = 128 * kKB * 2;  // 128 rows (or columns) of a stag
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// Named ids per row up to which the forward also takes their logits, and the
+// backward their part of dx, in plain fp32. More of them average the errors
+// that this is about, and their rows of W would cost more than the products
+// hide.
+constexpr int kFewNamed = 4;
 constexpr int kPairs = 74;            // CTA pairs of a full persistent grid (148 SMs)
 
 constexpr int kEpiWarps = 8;
@@ -119,6 +126,9 @@ struct Params {
   float* named;          // LSE: [kept row][K] z at the row's ids
   float* exact;          // the same from plain fp32 sums, for few ids per row, or null
   int row_pitch;
+  // what rounding dz to bf16 takes from the row's named columns, by kept row,
+  // where they are few: dx gets it back times their rows of W (or null)
+  float* rest;
   const float* acc;      // fp32 sums of dx, slot_rows(kept) rows per split
   __nv_bfloat16* dx;
   // zero at launch: [0] the next unit; then counters, in epilogue warps: per
@@ -428,6 +438,14 @@ __device__ __forceinline__ void load_operand(const CUtensorMap* m, bool mn, bool
   }
 }
 
+// s += g times four bf16 values.
+__device__ __forceinline__ void add_scaled4(float4& s, float g, uint2 v) {
+  s.x = fmaf(g, __uint_as_float(v.x << 16), s.x);
+  s.y = fmaf(g, __uint_as_float(v.x & 0xffff0000u), s.y);
+  s.z = fmaf(g, __uint_as_float(v.y << 16), s.z);
+  s.w = fmaf(g, __uint_as_float(v.y & 0xffff0000u), s.w);
+}
+
 // A teacher's list of one row, from the entry that the current 128 columns
 // begin with; `next` is the id there (INT_MAX past the last one of these
 // columns) and the one behind it is already on its way.
@@ -655,12 +673,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = next_unit(n + 1, un);
       }
     }
-  } else if (warp == 2 + kEpiWarps && rank == 0) {
+  } else if (kBwd && warp == 2 + kEpiWarps) {
     // ---------------- hand-out of units to both CTAs ----------------
     // A warp of its own: taking a number and finding its unit are long chains
     // that would hold up the loads.
     int wants = 0;
-    for (int n = 0; kBwd; ++n) {
+    for (int n = 0; rank == 0; ++n) {
       const int t = n % kTickets;
       if (!warp_wait_cl(bar(bTkEmpty + t), ((n / kTickets) & 1) ^ 1, abort_flag)) break;
       unsigned u = 0;
@@ -682,22 +700,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     // plain fp32, four at a time, eight lanes each, beside the products: the
     // loss is a difference of logits, and the tensor core's sums, cut instead
     // of rounded, would leave 1e-6 to 3e-6 of it.
-    if (!kBwd && p.exact) {
+    if (p.exact) {
       const int c8 = p.C / 8, sub = lane & 7;
-      const long items = (long)kept * p.K;
-      for (long i0 = (long)(blockIdx.x >> 1) * 4; i0 < items; i0 += (long)(gridDim.x >> 1) * 4) {
-        const long i = i0 + (lane >> 3);
+      const long items = (long)kept * p.K, step = (long)gridDim.x * 4;
+      auto find = [&](long i, int& row, int& id) {
+        row = 0;
+        id = -1;
+        if (i >= items) return;
         const int m = (int)(i / p.K);
-        int row = 0, id = -1;
-        if (i < items) {
-          row = p.n_kept ? p.row_of[m] : m;
-          id = p.ids[(size_t)row * p.K + (int)(i - (long)m * p.K)];
-        }
+        row = p.n_kept ? p.row_of[m] : m;
+        id = p.ids[(size_t)row * p.K + (int)(i - (long)m * p.K)];
+      };
+      long i = (long)blockIdx.x * 4 + (lane >> 3);
+      int row, id, next_row, next_id;
+      find(i, row, id);
+      for (; __any_sync(0xffffffffu, i < items); i += step, row = next_row, id = next_id) {
+        find(i + step, next_row, next_id);  // on its way during this one
         float s0 = 0.f, s1 = 0.f;
         if ((unsigned)id < (unsigned)p.V) {
           const uint4* xr = p.x + (size_t)row * c8;
           const uint4* wr = p.w + (size_t)id * c8;
-#pragma unroll 4
+#pragma unroll 8
           for (int q = sub; q < c8; q += 8) {
             const uint4 a = xr[q], b = wr[q];
             const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
@@ -896,7 +919,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               while (nm.next < cc + 32) {
                 const int e = nm.next - cc;
                 const uint32_t at = mine + (((e >> 2) ^ sw) << 4) + (e & 3) * 4;
-                st_shared_f32(at, fmaf(-cb, share[nm.pos], ld_shared_f32(at)));
+                const float d = fmaf(-cb, share[nm.pos], ld_shared_f32(at));
+                st_shared_f32(at, d);
+                if (p.rest)  // of an id named again, the last one's counts
+                  p.rest[(size_t)m * p.K + nm.pos] =
+                      nm.then == nm.next ? 0.f : d - __bfloat162float(__float2bfloat16_rn(d));
                 nm.advance();
               }
 #pragma unroll
@@ -905,9 +932,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
             }
           } else if (__any_sync(0xffffffffu, (unsigned)(target - 32 * c) < 32u)) {
+            float d = 0.f;
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (target == 32 * c + e) t[e] -= cb;
+              if (target == 32 * c + e) d = t[e] -= cb;
+            if ((unsigned)(target - 32 * c) < 32u)
+              p.rest[m] = d - __bfloat162float(__float2bfloat16_rn(d));
           }
           // rows that are not kept and columns past the vocabulary are zeros:
           // they are K values of the products that read this buffer
@@ -946,33 +976,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (is_dx)
           split_dx(((kept + kTile - 1) / kTile) * ((p.C + kTile - 1) / kTile),
                    (min(p.piece, p.V) + kKB - 1) / kKB, splits, kb_per);
-        const bool direct = is_dx && last && splits == 1;  // the sum ends here: straight to dx
         const bool f32 = is_dx || p.dw_f32;
         const CUtensorMap* mo = is_dx ? &maps.dx_out : &maps.dw_out;
         const int slot = slot_rows(kept);
         const int out_row = is_dx ? un.split * slot + row0 : v0 + row0;
         const int out_rows = is_dx ? kept : vn;  // rows of the job that exist
-        const int row = direct && m < kept ? p.row_of[m] : 0;
         if (__shfl_sync(0xffffffffu, owed != nullptr, 0)) settle();
-        uint32_t vv[2][32];
-        tmem_ld32(src, vv[0]);
+        if (is_dx && last && splits == 1) {
+          // the sum ends here: the earlier pieces', this one's, and what the
+          // rounding of dz took go straight to dx, by way of the staging, so
+          // that eight lanes read and write a row (a row per lane took 20 us
+          // at the end of the call, this 10)
+          const int row = m < kept ? p.row_of[m] : 0;
+          float rest[kFewNamed];
+          int id[kFewNamed];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int cs = col0 + 32 * c;
-          tmem_wait_ld();
-          if (c < 3) tmem_ld32(src + 32 * (c + 1), vv[(c + 1) & 1]);
-          else release();
-          uint32_t* v = vv[c & 1];
-          if (un.nkb == 0) {  // no rows kept: nothing was multiplied
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = 0u;
+          for (int k = 0; k < kFewNamed; ++k) {
+            rest[k] = 0.f;
+            id[k] = 0;
+            if (p.rest && k < p.K && m < kept) {
+              const int named = p.ids[(size_t)row * p.K + k];
+              if ((unsigned)named < (unsigned)p.V) {
+                id[k] = named;
+                rest[k] = __ldcg(p.rest + (size_t)m * p.K + k);
+              }
+            }
           }
-          if (cs >= p.C || row0 >= out_rows) continue;  // uniform in the warp
-          if (direct) {
-            // by way of the staging, so that eight lanes read and write a row:
-            // a row per lane took 20 us at the end of the call
+          const int quad = lane & 7;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const int cq = col0 + 32 * c + 4 * quad;
             float4 sum[8];
-            const int quad = lane & 7, cq = cs + 4 * quad;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int r = 4 * i + (lane >> 3);
@@ -980,6 +1014,26 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (un.p > 0 && row0 + r < kept && cq < p.C)
                 sum[i] = __ldcg(reinterpret_cast<const float4*>(p.acc + (size_t)(row0 + r) * p.C + cq));
             }
+#pragma unroll
+            for (int k = 0; k < kFewNamed; ++k) {
+              if (!p.rest || k >= p.K) break;
+              uint2 wv[8];  // rows of W (row 0 where there is nothing to add): all on their way
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int col = __shfl_sync(0xffffffffu, id[k], 4 * i + (lane >> 3));
+                wv[i] = *reinterpret_cast<const uint2*>(
+                    reinterpret_cast<const __nv_bfloat16*>(p.w) + (size_t)col * p.C + min(cq, p.C - 4));
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float g = __shfl_sync(0xffffffffu, rest[k], 4 * i + (lane >> 3));
+                if (g != 0.f) add_scaled4(sum[i], g, wv[i]);
+              }
+            }
+            uint32_t v[32];
+            tmem_ld32(src + 32 * c, v);
+            tmem_wait_ld();
+            if (c == 3) release();
             reuse_stage();
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -997,8 +1051,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                                pack_bf16(sum[i].z + f.z, sum[i].w + f.w));
             }
             __syncwarp();
-            continue;
           }
+          if (more) fetch_named(nu);
+          un = nu;
+          continue;
+        }
+        uint32_t vv[2][32];
+        tmem_ld32(src, vv[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int cs = col0 + 32 * c;
+          tmem_wait_ld();
+          if (c < 3) tmem_ld32(src + 32 * (c + 1), vv[(c + 1) & 1]);
+          else release();
+          uint32_t* v = vv[c & 1];
+          if (un.nkb == 0) {  // no rows kept: nothing was multiplied
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = 0u;
+          }
+          if (cs >= p.C || row0 >= out_rows) continue;  // uniform in the warp
           if (f32 || (c & 1) == 0) reuse_stage();
           const uint32_t my_row = stage + lane * 128;
           if (f32) {
