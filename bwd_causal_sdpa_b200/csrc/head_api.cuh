@@ -195,7 +195,7 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
 
   if (K) {
     const unsigned blocks = (unsigned)std::min<long>((N + kTeacherWarps - 1L) / kTeacherWarps, 148L * 16);
-    const size_t smem = (size_t)kTeacherWarps * K * 8;
+    const size_t smem = (size_t)kTeacherWarps * ((K + 3) / 4) * 32;
     uint16_t* first = (uint16_t*)(ws + hp.first);
     if (c.t_dtype == ATTN_F32)
       ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_teacher_kernel<float>, blocks, 32 * kTeacherWarps, smem, st,

@@ -143,10 +143,11 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
                         float* __restrict__ share, uint16_t* __restrict__ first, int first_pitch,
                         float* __restrict__ entropy, int* __restrict__ flags, int N, int V, int K) {
   pdl_wait_and_trigger();
-  extern __shared__ int smem_teacher[];
+  extern __shared__ __align__(16) int smem_teacher[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int* key = smem_teacher + warp * 2 * K;
-  int* sorted = key + K;
+  const int K4 = (K + 3) / 4;
+  int* key = smem_teacher + warp * 8 * K4;  // 16-byte aligned
+  int* sorted = key + 4 * K4;
   for (int r = blockIdx.x * kTeacherWarps + warp; r < N; r += gridDim.x * kTeacherWarps) {
     const int* in = t_idx + (size_t)r * K;
     const TT* tl = t_logit + (size_t)r * K;
@@ -163,6 +164,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
         top = fmaxf(top, t);
       }
     }
+    if (lane < 4 * K4 - K) key[K + lane] = INT_MAX;
     if (bad) report_status(ATTN_EDEVICE_INPUT);
     top = warp_max(top);
     nan = __any_sync(0xffffffffu, nan);
@@ -184,9 +186,12 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
       }
       int rank = 0;
 #pragma unroll 4
-      for (int i = 0; i < K; ++i) {
-        const int other = key[i];
-        rank += (other < mine || (other == mine && i < k)) ? 1 : 0;
+      for (int i = 0; i < K4; ++i) {
+        const int4 o = reinterpret_cast<const int4*>(key)[i];
+        const int other[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          rank += (other[e] < mine || (other[e] == mine && 4 * i + e < k)) ? 1 : 0;
       }
       sorted[rank] = mine;
       ids[(size_t)r * K + rank] = mine;

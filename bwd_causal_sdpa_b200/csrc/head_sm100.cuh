@@ -447,26 +447,42 @@ __device__ __forceinline__ void add_scaled4(float4& s, float g, uint2 v) {
 }
 
 // A teacher's list of one row, from the entry that the current 128 columns
-// begin with; `next` is the id there (INT_MAX past the last one of these
-// columns) and the one behind it is already on its way.
+// begin with: the ids of the next entries (INT_MAX past the last one of these
+// columns), with their shares in the backward. kDeep of them are on their way:
+// a row with many entries in a tile takes them one after the other.
+template <bool kShares>
 struct Named {
+  static constexpr int kDeep = 4;
   const int* ids;
-  int pos, end, next, then;
+  const float* shares;
+  int pos, end, id[kDeep];
+  float share[kDeep];
+  __device__ __forceinline__ void load(int d, int at) {
+    id[d] = at < end ? ids[at] : INT_MAX;
+    if constexpr (kShares) share[d] = at < end ? shares[at] : 0.f;
+  }
   __device__ __forceinline__ void none() {
     pos = end = 0;
-    next = then = INT_MAX;
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) id[d] = INT_MAX;
   }
-  __device__ __forceinline__ void list(const int* row_ids, int from, int to) {
+  __device__ __forceinline__ void list(const int* row_ids, const float* row_shares, int from,
+                                       int to) {
     ids = row_ids;
+    shares = row_shares;
     pos = from;
     end = to;
-    next = from < to ? ids[from] : INT_MAX;
-    then = from + 1 < to ? ids[from + 1] : INT_MAX;
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) load(d, from + d);
   }
   __device__ __forceinline__ void advance() {
     ++pos;
-    next = then;
-    then = pos + 1 < end ? ids[pos + 1] : INT_MAX;
+#pragma unroll
+    for (int d = 0; d + 1 < kDeep; ++d) {
+      id[d] = id[d + 1];
+      share[d] = share[d + 1];
+    }
+    load(kDeep - 1, pos + kDeep - 1);
   }
 };
 
@@ -793,13 +809,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m = row0 + lane;
       const int col0 = un.tn * kTile + half * 128;  // within the piece, or of C
       const int v0 = un.p * p.piece, vn = min(p.piece, p.V - v0), vend = v0 + vn;
-      Named nm;
+      Named<kBwd> nm;
       nm.none();
-      const float* share = nullptr;
-      if (p.share && n_from < n_to) {
-        nm.list(p.ids + (size_t)rp.id * p.K, n_from, n_to);
-        share = p.share + (size_t)rp.id * p.K;
-      }
+      if (p.share && n_from < n_to)
+        nm.list(p.ids + (size_t)rp.id * p.K, p.share + (size_t)rp.id * p.K, n_from, n_to);
       const float lse2 = rp.lse2, ca = rp.ca, cb = rp.cb;
       // without a list: within these columns or not
       const int target = m < kept ? rp.id - (v0 + col0) : -1;
@@ -831,13 +844,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int cc = v0 + col0 + 32 * c;
           // a teacher's ids among these 32 columns: each lane looks its row's up
           // in its own 128 bytes of the staging (swizzled in 16-byte groups)
-          if (__any_sync(0xffffffffu, nm.next < cc + 32)) {
+          if (__any_sync(0xffffffffu, nm.id[0] < cc + 32)) {
             const uint32_t mine = stage + lane * 128;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               st_shared_v4(mine + ((e ^ sw) << 4), t[4 * e], t[4 * e + 1], t[4 * e + 2], t[4 * e + 3]);
-            while (nm.next < cc + 32) {
-              const int e = nm.next - cc;
+            while (nm.id[0] < cc + 32) {
+              const int e = nm.id[0] - cc;
               p.named[(size_t)m * p.K + nm.pos] =
                   ld_shared_f32(mine + (((e >> 2) ^ sw) << 4) + (e & 3) * 4) * p.inv_tau;
               nm.advance();
@@ -907,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (p.share) {
             // a teacher's shares, in a staging buffer that no store reads
-            if (__any_sync(0xffffffffu, nm.next < cc + 32)) {
+            if (__any_sync(0xffffffffu, nm.id[0] < cc + 32)) {
               if (lane == 0) bulk_wait_group_read0();
               __syncwarp();
               const uint32_t mine = (stage ^ 4096) + lane * 128;
@@ -916,14 +929,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st_shared_v4(mine + ((e ^ sw) << 4), __float_as_uint(t[4 * e]),
                              __float_as_uint(t[4 * e + 1]), __float_as_uint(t[4 * e + 2]),
                              __float_as_uint(t[4 * e + 3]));
-              while (nm.next < cc + 32) {
-                const int e = nm.next - cc;
+              while (nm.id[0] < cc + 32) {
+                const int e = nm.id[0] - cc;
                 const uint32_t at = mine + (((e >> 2) ^ sw) << 4) + (e & 3) * 4;
-                const float d = fmaf(-cb, share[nm.pos], ld_shared_f32(at));
+                const float d = fmaf(-cb, nm.share[0], ld_shared_f32(at));
                 st_shared_f32(at, d);
                 if (p.rest)  // of an id named again, the last one's counts
                   p.rest[(size_t)m * p.K + nm.pos] =
-                      nm.then == nm.next ? 0.f : d - __bfloat162float(__float2bfloat16_rn(d));
+                      nm.id[1] == nm.id[0] ? 0.f : d - __bfloat162float(__float2bfloat16_rn(d));
                 nm.advance();
               }
 #pragma unroll
