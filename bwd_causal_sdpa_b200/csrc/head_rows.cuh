@@ -290,7 +290,9 @@ __global__ void __launch_bounds__(kLossThreads)
         const int id = ids[(size_t)r * K + k];
         const bool again = k > 0 && ids[(size_t)r * K + k - 1] == id;
         const float diff = exact[own + k] - named[own + k];
-        if ((unsigned)id < (unsigned)V && !again && diff != 0.f) d += expf(named[own + k] - l) * diff;
+        // (both may be infinite)
+        if ((unsigned)id < (unsigned)V && !again && isfinite(diff) && diff != 0.f)
+          d += expf(named[own + k] - l) * diff;
       }
     for (int o = 4; o < 32; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
     l += d;

@@ -231,6 +231,34 @@ def test_nan_and_infinity_in_kept_rows_stay_in_their_rows():
         assert torch.equal(a[rest], b[rest])
 
 
+@pytest.mark.parametrize("N", [40, 300])
+def test_a_target_whose_logit_overflows(N):
+    """A target at -inf: its loss is inf, its row's lse and every other row are
+    what they are without it."""
+    import torch
+
+    from bwd_causal_sdpa_b200 import ATTN_OK
+    from bwd_causal_sdpa_b200.runner import HeadRunner
+
+    w = make_head_workload(head_config_by_name("head_small"), N=N, left_out=0.0)
+    w.w[:, :2] = 0.0
+    w.w[5, :2] = -1.0
+    w.x[:, :2] = 0.0
+    w.target[w.target == 5] = 6
+    clean, _ = _check(w)
+    w.x[3, :2] = np.float32(2.0**127)
+    w.target[3] = 5
+    r = HeadRunner(w)
+    r.forward()
+    assert r.status() == ATTN_OK
+    z = w.x[3, 2:].astype(np.float64) @ w.w[np.arange(w.cfg.V) != 5, 2:].astype(np.float64).T
+    want = np.log(np.exp(z - z.max()).sum()) + z.max()
+    assert r.loss[3].item() == np.inf
+    assert abs(r.lse[3].item() - want) <= 1e-5 * (1 + abs(want))
+    rest = torch.arange(N, device="cuda") != 3
+    assert torch.equal(r.loss[rest], clean.loss[rest]) and torch.equal(r.lse[rest], clean.lse[rest])
+
+
 def test_same_call_same_bits_and_nothing_behind_is_written():
     """Outputs inside larger buffers: what lies behind them stays."""
     import torch
