@@ -17,7 +17,7 @@ constexpr size_t kDzBytes = (size_t)96 << 20;
 constexpr long kDzMinCols = 2048;
 
 struct HeadPlan {
-  int rows_pad = 0, piece = 0, pieces = 0, parts = 0;
+  int rows_pad = 0, piece = 0, pieces = 0, lw = 0, parts = 0;
   size_t n_kept = 0, ctl = 0, row_of = 0, pos = 0, par = 0, xc = 0, ids = 0, share = 0, entropy = 0, flags = 0, first = 0;
   size_t part = 0, named = 0, exact = 0;  // forward
   size_t dz[head100::kDzBuffers] = {}, acc = 0, rest = 0;  // backward
@@ -53,6 +53,12 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
   p.pieces = (int)((V + cols - 1) / cols);
   p.piece = (int)(((V + p.pieces - 1) / p.pieces + kTile - 1) / kTile * kTile);
   p.pieces = (V + p.piece - 1) / p.piece;
+  // Narrow logits tiles, half as long, where they still find a pair each (one
+  // row tile against 5306 ids, width 888: 42 units of 3600 cycles for 21 of
+  // 7200). Beyond, W bounds the time, and its boxes of 64 rows move slower: 33
+  // rows against 24576 ids took 34 us narrow, 26 wide.
+  const long narrow = (long)(p.rows_pad / kTile) * ((std::min(p.piece, V) + 127) / 128);
+  p.lw = narrow <= kPairs ? 128 : 256;
   p.n_ctl = ctl_words(V, p.pieces);
   p.n_kept = take(4);
   p.ctl = take((size_t)p.n_ctl * 4);
@@ -64,12 +70,12 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
     p.ids = take((size_t)N * K * 4);
     p.share = take((size_t)N * K * 4);
     p.flags = take((size_t)N * 4);
-    p.first_pitch = 2 * ((V + kTile - 1) / kTile) + 1;
+    p.first_pitch = 2 * ((V + p.lw - 1) / p.lw) + 1;
     p.first = take((size_t)N * p.first_pitch * 2);
     if (!bwd) p.entropy = take((size_t)N * 4);
   }
   if (!bwd) {
-    p.parts = 2 * ((V + kTile - 1) / kTile);
+    p.parts = 2 * ((V + p.lw - 1) / p.lw);
     p.part = take((size_t)p.parts * p.rows_pad * sizeof(float2));
     p.named = take((size_t)N * std::max(K, 1) * 4);
     if (K <= kFewNamed) p.exact = take((size_t)N * std::max(K, 1) * 4);
@@ -161,18 +167,18 @@ int head_check(const HeadCall& c, void* ws, size_t ws_bytes) {
   return ATTN_OK;
 }
 
-template <bool kBwd>
+template <bool kBwd, int kLw>
 int head_gemm(const head100::Maps& maps, const head100::Params& p, cudaStream_t st) {
   using namespace head100;
   static bool smem_done[64];
-  if (!ensure_smem(head_gemm_kernel<kBwd>, kSmAlloc, smem_done)) return ATTN_ECUDA;
+  if (!ensure_smem(head_gemm_kernel<kBwd, kLw>, kSmAlloc, smem_done)) return ATTN_ECUDA;
   // pairs beyond the units that any number of kept rows gives would be idle
   const Sched s = make_sched(p, p.N);
   long units = kBwd ? kPairs : s.dz(0);
   // the fp32 logits of few named ids want warps, four of them each (two a pair)
   if (!kBwd && p.exact) units = std::max(units, ((long)p.N * p.K + 7) / 8);
   const unsigned pairs = (unsigned)std::min<long>(units, kPairs);
-  ATTN_LAUNCH(KK_HEAD_GEMM, st, pdl_cluster_launch(head_gemm_kernel<kBwd>, dim3(2 * pairs), kThreads,
+  ATTN_LAUNCH(KK_HEAD_GEMM, st, pdl_cluster_launch(head_gemm_kernel<kBwd, kLw>, dim3(2 * pairs), kThreads,
                                                    kSmAlloc, st, 2u, maps, p));
   return launch_status();
 }
@@ -200,11 +206,11 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
     if (c.t_dtype == ATTN_F32)
       ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_teacher_kernel<float>, blocks, 32 * kTeacherWarps, smem, st,
                                                c.t_idx, (const float*)c.t_logit, inv_tau, c.dloss, c.dlse,
-                                               ids, share, first, hp.first_pitch, entropy, flags, N, V, K));
+                                               ids, share, first, hp.first_pitch, hp.lw / 2, entropy, flags, N, V, K));
     else
       ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_teacher_kernel<__nv_bfloat16>, blocks, 32 * kTeacherWarps, smem, st,
                                                c.t_idx, (const __nv_bfloat16*)c.t_logit, inv_tau, c.dloss, c.dlse,
-                                               ids, share, first, hp.first_pitch, entropy, flags, N, V, K));
+                                               ids, share, first, hp.first_pitch, hp.lw / 2, entropy, flags, N, V, K));
   }
   // A forward of one row tile costs the same for any number of kept rows, and
   // its rows do not meet: it goes without the row pass (4 of 27 us at one row).
@@ -249,6 +255,7 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   p.ctl = ra.ctl;
   p.piece = hp.piece;
   p.pieces = hp.pieces;
+  p.lw = hp.lw;
   p.ids = K ? ids : c.target;
   p.share = share;
   p.first = K ? (const uint16_t*)(ws + hp.first) : nullptr;
@@ -256,14 +263,15 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   p.row_pitch = hp.rows_pad;
   if (!head_map(&maps.x_k, c.x, false, N, C, C, 128) ||
       !head_map(&maps.xc_k, xc, false, hp.rows_pad, C, C, 128) ||
-      !head_map(&maps.w_k, c.w, false, V, C, C, 128))
+      !head_map(&maps.w_k, c.w, false, V, C, C, hp.lw / 2))
     return ATTN_ECUDA;
 
   if (!c.bwd) {
     p.part = (float2*)(ws + hp.part);
     p.named = (float*)(ws + hp.named);
     p.exact = K <= kFewNamed ? (float*)(ws + hp.exact) : nullptr;
-    if (int rc = head_gemm<false>(maps, p, st)) return rc;
+    if (int rc = hp.lw == 128 ? head_gemm<false, 128>(maps, p, st) : head_gemm<false, 256>(maps, p, st))
+      return rc;
     ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_loss_kernel, (unsigned)((N + kLossThreads / 8 - 1) / (kLossThreads / 8)),
                                              kLossThreads, 0, st, p.part, p.named, p.exact, p.ids, share, entropy,
                                              whole ? nullptr : pos, c.target, flags, c.loss, c.lse_out, N,
@@ -292,7 +300,8 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
          head_map(&maps.dz_out[b], dz, false, hp.rows_pad, hp.piece, hp.piece, 32);
   }
   if (!ok) return ATTN_ECUDA;
-  if (int rc = head_gemm<true>(maps, p, st)) return rc;
+  if (int rc = hp.lw == 128 ? head_gemm<true, 128>(maps, p, st) : head_gemm<true, 256>(maps, p, st))
+    return rc;
   const long n8 = (long)N * (C / 8);
   ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_dx_kernel, (unsigned)std::min<long>((n8 + 255) / 256, 148L * 8),
                                            256, 0, st, p.acc, row_of, n_kept, p.rest, p.ids, p.w, (uint4*)c.dx,

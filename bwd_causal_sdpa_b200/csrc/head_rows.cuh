@@ -129,8 +129,8 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowsArgs a
 
 // The teacher's list of one row per warp: q = softmax of t / tau over the
 // entries present (0 <= id < V), ids sorted ascending with their q (absent
-// ones last, id INT_MAX, q 0), how many of them lie below each multiple of 128
-// columns, sum q log q, and whether the row counts (some entry above -inf, and
+// ones last, id INT_MAX, q 0), how many of them lie below each multiple of
+// first_cols columns, sum q log q, and whether the row counts (some entry above -inf, and
 // an upstream gradient that is not zero). The sort is by rank (K comparisons
 // per entry): stable, so equal ids keep their order. The maximum is taken off
 // before the division by tau: entries at the type's lowest value then differ
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
     head_teacher_kernel(const int* __restrict__ t_idx, const TT* __restrict__ t_logit,
                         float inv_tau, const float* __restrict__ dloss,
                         const float* __restrict__ dlse, int* __restrict__ ids,
-                        float* __restrict__ share, uint16_t* __restrict__ first, int first_pitch,
+                        float* __restrict__ share, uint16_t* __restrict__ first, int first_pitch, int first_cols,
                         float* __restrict__ entropy, int* __restrict__ flags, int N, int V, int K) {
   pdl_wait_and_trigger();
   extern __shared__ __align__(16) int smem_teacher[];
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
     __syncwarp();
     for (int b = lane; b < first_pitch; b += 32) {
       int lo = 0, hi = K;
-      const long col = 128L * b;
+      const long col = (long)first_cols * b;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (sorted[mid] < col) lo = mid + 1;

@@ -4,9 +4,10 @@
 //
 // Forward. Row n needs lse_n = log sum_v exp z[n][v] and z at the few ids its
 // loss names (the target, or a teacher's list). The logits are formed one
-// 256 x 256 tile at a time in tensor memory; the epilogue keeps, per row and
-// 128 columns, the running maximum and sum of exponentials (fp32, base 2) and
-// the named logits, 8 bytes per 128 logits instead of the logits.
+// 256 x 256 tile at a time in tensor memory (256 x 128 where that fills more
+// pairs of CTAs); the epilogue keeps, per row and half a tile, the running
+// maximum and sum of exponentials (fp32, base 2) and the named logits, 8 bytes
+// per 128 (64) logits instead of the logits.
 //
 // Backward. With p = exp(z - lse) the gradient of the logits is
 //     dz[n][v] = (dloss_n + dlse_n) / tau * p[n][v] - dloss_n / tau * q[n][v],
@@ -91,7 +92,8 @@ static_assert(kSmTickets % 16 == 0 && kSmStage % 1024 == 0, "alignment");
 enum Kind : int { LSE = 0, DZ = 1, DX = 2, DW = 3, END = 4 };
 
 struct Maps {
-  // operand loads: _k with K contiguous (boxes of 64 K x 128 rows), _mn with
+  // operand loads: _k with K contiguous (boxes of 64 K x 128 rows; W's of 64
+  // rows for narrow logits tiles), _mn with
   // the row index contiguous (boxes of 64 rows x 64 K, two of them in one box
   // when the extent is a multiple of 64)
   CUtensorMap x_k, xc_k, w_k, x_mn, xc_mn, w_mn, dz_k[kDzBuffers], dz_mn[kDzBuffers];
@@ -111,6 +113,7 @@ struct Params {
   int N, V, C;
   int K;                 // named ids per row (1: the target)
   int piece, pieces;     // vocabulary rows per piece (all of V in the forward)
+  int lw;                // columns of a logits tile: 256, or 128 where those are few
   int c_blocks;          // C % 64 == 0: _mn maps of x and W take both 64-wide blocks in one box
   int dw_f32;
   float inv_tau;
@@ -120,9 +123,9 @@ struct Params {
   const RowPar* par;     // by kept row
   const int* ids;        // [N][K]: the targets, or a teacher's ids, ascending
   const float* share;    // [N][K] q, or null (1 at the target)
-  const uint16_t* first; // [N][first_pitch] entries with an id below 128 b (with share)
+  const uint16_t* first; // [N][first_pitch] entries with an id below b lw / 2 (with share)
   int first_pitch;
-  float2* part;          // LSE: [2 tiles][row_pitch] maximum (base 2), sum
+  float2* part;          // LSE: [2 logits tiles][row_pitch] maximum (base 2), sum
   float* named;          // LSE: [kept row][K] z at the row's ids
   float* exact;          // the same from plain fp32 sums, for few ids per row, or null
   int row_pitch;
@@ -162,7 +165,7 @@ __host__ __device__ inline int slot_rows(int kept) { return (kept + kTile - 1) /
 
 // The units of a call, for `kept` rows.
 struct Sched {
-  int pieces, piece, V;
+  int pieces, piece, V, lw;
   int tm, tc;          // tiles of kept rows, of C
   int kb_c, kb_n;      // K blocks of the logits, of dW
   int splits, kb_per;  // of dx over a whole piece
@@ -173,7 +176,8 @@ struct Sched {
   // a shorter last piece keeps the parts' length: it adds into accumulators
   // that the first piece has written
   __host__ __device__ int splits_of(int p) const { return (kb_v(p) + kb_per - 1) / kb_per; }
-  __host__ __device__ int dz(int p) const { return tm * tv(p); }
+  __host__ __device__ int tl(int p) const { return (cols(p) + lw - 1) >> (lw == kTile ? 8 : 7); }
+  __host__ __device__ int dz(int p) const { return tm * tl(p); }
   __host__ __device__ int dw(int p) const { return tv(p) * tc; }
   __host__ __device__ int dx(int p) const { return tm * tc * splits_of(p); }
 };
@@ -182,6 +186,7 @@ __host__ __device__ inline Sched make_sched(const Params& p, int kept) {
   s.pieces = p.pieces;
   s.piece = p.piece;
   s.V = p.V;
+  s.lw = p.lw;
   s.tm = (kept + kTile - 1) / kTile;
   s.tc = (p.C + kTile - 1) / kTile;
   s.kb_c = (p.C + kKB - 1) / kKB;
@@ -221,7 +226,7 @@ __device__ __forceinline__ Unit find_unit(const Sched& s, int u) {
     o.kind = kind;
     o.p = p;
     o.nkb = s.kb_c;
-    band_tile(u, s.tm, s.tv(p), kLogitsBand, o.tm, o.tn);
+    band_tile(u, s.tm, s.tl(p), kLogitsBand, o.tm, o.tn);
   };
   if constexpr (!kBwd) {
     if (u < s.dz(0)) logits(LSE, 0);
@@ -393,17 +398,21 @@ __device__ __forceinline__ bool warp_count(const unsigned* c, unsigned want,
   return __all_sync(0xffffffffu, wait_count(c, want, abort_flag));
 }
 
-// Bounded wait for the counters of tiles t0 to t1, a lane per tile; also looks
-// at those behind (up to `end`): `to` is one past the last of the tiles from t0
-// on that were there without a gap.
+// Bounded wait for dz of the vocabulary tiles t0 to t1, a lane per tile; also
+// looks at those behind (up to `end`): `to` is one past the last of the tiles
+// from t0 on that were there without a gap. A tile's counter gets one from every
+// epilogue warp of its logits tiles, two of these per row tile where they are
+// narrow (one where the vocabulary ends in the tile's first half).
 __device__ __forceinline__ bool wait_tiles(const unsigned* done, int t0, int t1, int end,
-                                           unsigned want, int lane, int& to,
+                                           const Sched& sc, int lane, int& to,
                                            volatile int* abort_flag) {
   const long long start = clock64();
   bool ok = true;
   to = t0;
   while (to <= t1) {
     const int t = to + lane;
+    const int left = sc.V - t * kTile;
+    const unsigned want = 2u * kEpiWarps * sc.tm * (left > sc.lw && sc.lw < kTile ? 2 : 1);
     const bool there = t < end && ld_acquire(done + t) >= want;
     const unsigned gap = ~__ballot_sync(0xffffffffu, there);
     to += gap ? __ffs(gap) - 1 : 32;
@@ -486,9 +495,10 @@ struct Named {
   }
 };
 
-// kBwd: the backward's units, else the forward's. Two kernels, so that neither
-// carries the other's epilogues.
-template <bool kBwd>
+// kBwd: the backward's units, else the forward's. kLw: columns of a logits
+// tile. Kernels of their own, so that none carries another's epilogues (a width
+// known at run time cost short tiles up to 11 %).
+template <bool kBwd, int kLw>
 __global__ void __launch_bounds__(kThreads, 1)
     head_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -581,13 +591,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap *ma, *mb;
       bool a_mn = false, b_mn = true, b_one = p.c_blocks != 0;
       const int v0 = un.p * p.piece, buf = un.p % kDzBuffers;
-      int bk = 0, brow = un.tn * kTile + rank * 128;
+      int bk = 0, brow = un.tn * kTile + rank * 128, bytes = 2 * kStageBytes;
       const int arow = un.tm * kTile + rank * 128;
       if (!kBwd || un.kind == DZ) {
         ma = all ? &maps.x_k : &maps.xc_k;
         mb = &maps.w_k;
         b_mn = false;
-        brow += v0;
+        brow = v0 + un.tn * kLw + rank * (kLw / 2);
+        bytes = 2 * (kOperandBytes + kKB * kLw);  // lw / 2 rows of 128 bytes
         const int q = un.p - kDzBuffers;  // the piece whose dz this one overwrites
         if (q > used_ok) {
           if (!warp_count(dz_used + q, 2u * (sc.dw(q) + sc.dx(q)), abort_flag)) break;
@@ -607,8 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t0 = v0 / kTile + (un.kind == DW ? un.tm : un.kb0 / 4);
         const int t1 = v0 / kTile + (un.kind == DW ? un.tm : (un.kb0 + un.nkb - 1) / 4);
         if (t0 < dz_from || t1 >= dz_to) {
-          ok = wait_tiles(dz_done, t0, t1, v0 / kTile + sc.tv(un.p), 2u * kEpiWarps * sc.tm, lane,
-                          dz_to, abort_flag);
+          ok = wait_tiles(dz_done, t0, t1, v0 / kTile + sc.tv(un.p), sc, lane, dz_to, abort_flag);
           dz_from = t0;
           if (!ok) break;
         }
@@ -625,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (el) {
           if (kBwd && rank == 0 && kb == un.nkb - 1 - kAhead) mbar_arrive(bar(bWant));
           // CTA 0's barrier counts the bytes of both CTAs' boxes
-          if (rank == 0) mbar_arrive_expect_tx(bar(bFull + s), 2 * kStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(bar(bFull + s), bytes);
           const uint32_t full = map_rank(bar(bFull + s), 0);
           const uint32_t dst = sb0 + kSmRing + s * kStageBytes;
           const int k0 = (un.kb0 + kb) * kKB;
@@ -652,7 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = next_unit(0, un);
       for (int n = 0; ok; ++n) {
         const bool a_mn = kBwd && un.kind == DW, b_mn = kBwd && un.kind >= DX;
-        const uint32_t idesc = idesc_f16(kTile, kTile, true, true, a_mn, b_mn);
+        const uint32_t idesc = b_mn ? idesc_f16(kTile, kTile, true, true, a_mn, b_mn)
+                                    : idesc_f16(kTile, kLw, true, true, false, false);
         // descriptors count in 16 bytes: 16 K values are 32 bytes along a row
         // of K, or 16 rows of 128 bytes
         const uint64_t a0 = a_mn ? mn_desc : k_desc;
@@ -755,9 +766,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------- epilogue: thread = TMEM lane = output row ----------------
-    // warp w reads lanes 32 (w % 4).. of columns 128 half..: two warps per lane quarter
+    // warp w reads lanes 32 (w % 4).. of one half of the columns: two warps per
+    // lane quarter
     const int sub = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16) + half * 128;
+    const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
+    constexpr int lhalf = kLw / 2, lchunks = kLw / 64;  // of a logits tile
     uint32_t stage = sb0 + kSmStage + (warp - 2) * 8192;  // of the two buffers, the next one
     const int sw = lane & 7;
     const float c2 = p.inv_tau * kLog2e;
@@ -793,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m = w.tm * kTile + rank * 128 + sub * 32 + lane;
       if (p.share && w.kind <= DZ && m < kept) {
         const uint16_t* f = p.first + (size_t)rp.id * p.first_pitch +
-                            (w.p * p.piece + w.tn * kTile + half * 128) / 128;
+                            (w.p * p.piece + w.tn * kLw) / lhalf + half;
         n_from = f[0];
         n_to = f[1];
       }
@@ -807,7 +820,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int a = n & 1;
       const int row0 = un.tm * kTile + rank * 128 + sub * 32;  // of this warp
       const int m = row0 + lane;
-      const int col0 = un.tn * kTile + half * 128;  // within the piece, or of C
+      const bool logits = !kBwd || un.kind == DZ;
+      // this warp's columns: within the piece, or of C
+      const int col0 = logits ? un.tn * kLw + half * lhalf : un.tn * kTile + half * 128;
       const int v0 = un.p * p.piece, vn = min(p.piece, p.V - v0), vend = v0 + vn;
       Named<kBwd> nm;
       nm.none();
@@ -830,15 +845,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_read(map_rank(bar(bAccEmpty + a), 0));
       };
-      const uint32_t src = tl + a * kTile;
+      const uint32_t src = tl + a * kTile + half * (logits ? lhalf : 128);
       if constexpr (!kBwd) {
         float mx = -INFINITY, sum = 0.f;
         uint32_t v[2][32];
         tmem_ld32(src, v[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < lchunks; ++c) {
           tmem_wait_ld();
-          if (c < 3) tmem_ld32(src + 32 * (c + 1), v[(c + 1) & 1]);
+          if (c + 1 < lchunks) tmem_ld32(src + 32 * (c + 1), v[(c + 1) & 1]);
           else release();
           const uint32_t* t = v[c & 1];
           const int cc = v0 + col0 + 32 * c;
@@ -903,9 +918,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 k2 = make_float2(c2, c2), l2 = make_float2(-lse2, -lse2),
                      a2 = make_float2(ca, ca);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < lchunks; ++c) {
           tmem_wait_ld();
-          if (c < 3) tmem_ld32(src + 32 * (c + 1), v[(c + 1) & 1]);
+          if (c + 1 < lchunks) tmem_ld32(src + 32 * (c + 1), v[(c + 1) & 1]);
           else release();
           const uint32_t* tv = v[c & 1];
           const int cc = v0 + col0 + 32 * c;
@@ -978,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             stage ^= 4096;
           }
         }
-        if (lane == 0) owed = dz_done + v0 / kTile + un.tn;
+        if (lane == 0) owed = dz_done + (v0 + un.tn * kLw) / kTile;
       } else {
         // dz of this unit has been read (by the products that this warp waited
         // for): its buffer may be overwritten, if a later piece does
