@@ -389,8 +389,8 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
  * attn_head_ce*; 0 for invalid sizes. The backward takes the vocabulary in
  * pieces, so its workspace does not grow with V: at most 3 x 96 MiB for dz up
  * to 24576 rows (3 x 4096 bytes a row beyond), plus the kept rows of x and the
- * fp32 sums of dx. (A teacher's lists add N (8 K + V / 64) bytes.) Pure host
- * function.
+ * fp32 sums of dx. (A teacher's lists add at most N (8 K + V / 32) bytes.) Pure
+ * host function.
  */
 size_t attn_head_workspace_bytes(int N, int V, int C, int K, int is_bwd);
 int attn_head_ce(const void* x, const void* w, const int32_t* target, float* loss, float* lse,

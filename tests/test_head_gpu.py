@@ -337,6 +337,45 @@ def test_streams_and_captured_graphs():
             assert torch.equal(getattr(r, n), t)
 
 
+def test_large_calls_at_once():
+    """Two steps whose units each fill the GPU, on streams of their own beside
+    an attention: the same bits as alone, whatever share of the SMs each gets."""
+    import torch
+
+    import bwd_causal_sdpa_b200 as A
+    from bwd_causal_sdpa_b200.runner import AttnRunner, HeadRunner
+
+    ws = [make_head_workload(head_config_by_name(n), N=N, V=V, C=C, left_out=0.1, seed=95)
+          for n, N, V, C in (("head_small", 4100, 20001, 256), ("head_distill_small", 3000, 9000, 520))]
+    names = ("loss", "lse", "dx", "dw")
+    alone = []
+    for w in ws:
+        r = HeadRunner(w)
+        r.forward()
+        r.backward()
+        assert r.status() == A.ATTN_OK
+        alone.append([getattr(r, n).clone() for n in names])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    rs = [HeadRunner(w, stream=s) for w, s in zip(ws, streams)]
+    at = AttnRunner(1, 8, 4096, 128, stream=streams[2])
+    for t in (at.q, at.k, at.v, at.do):
+        t.normal_()
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for r in rs:
+            r.forward()
+            r.backward()
+        at.forward()
+        at.backward()
+    torch.cuda.synchronize()
+    assert A.attn_get_status() == A.ATTN_OK
+    for r, ref in zip(rs, alone):
+        for n, t in zip(names, ref):
+            assert torch.equal(getattr(r, n), t), n
+    assert torch.isfinite(at.dq.float()).all()
+
+
 def test_output_projection_feeds_the_loss():
     """The end of a training step: o -> attn_out_proj -> attn_head_ce, and back
     through attn_head_ce_bwd and attn_out_proj_bwd, against the oracle's chain
