@@ -832,7 +832,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // without a list: within these columns or not
       const int target = m < kept ? rp.id - (v0 + col0) : -1;
       const uint32_t full = bar(bAccFull + a), par = (n >> 1) & 1;
-      if (!__all_sync(0xffffffffu, mbar_test(full, par))) settle();  // others may wait for it: never block owing
+      // others may wait for what this warp owes: it never blocks owing
+      if (!__all_sync(0xffffffffu, mbar_test(full, par))) settle();
       if (!warp_wait(full, par, abort_flag)) break;
       tc_fence_after();
       // the next unit, so that its rows' values arrive during this one
