@@ -13,6 +13,8 @@ namespace {
 // are in use) takes up to 96 MiB, or 2048 columns when the rows are many
 // (shorter pieces would add into dx more often than their products are worth).
 // 8192 rows of width 2048: 2.61 ms with 64 MiB, 2.55 with 96, 2.56 with 160.
+// With an fp32 dW a column takes both terms of dz, and the fewest columns are
+// half as many.
 constexpr size_t kDzBytes = (size_t)96 << 20;
 constexpr long kDzMinCols = 2048;
 
@@ -20,8 +22,9 @@ struct HeadPlan {
   int rows_pad = 0, piece = 0, pieces = 0, lw = 0, parts = 0;
   size_t n_kept = 0, ctl = 0, row_of = 0, pos = 0, par = 0, xc = 0, ids = 0, share = 0, entropy = 0, flags = 0, first = 0;
   size_t part = 0, named = 0, exact = 0;  // forward
-  size_t dz[head100::kDzBuffers] = {}, acc = 0, rest = 0;  // backward
-  long acc_rows = 0;
+  size_t dz[head100::kDzBuffers] = {}, lo[head100::kDzBuffers] = {}, acc = 0, rest = 0;  // backward
+  long acc_rows = 0, lo_blocks = 0;  // of 64 rows x 256 columns, in each of lo's buffers
+  int lo_rows = 0;
   int n_ctl = 0, first_pitch = 0;
   size_t total = 0;
 };
@@ -32,11 +35,11 @@ bool head_sizes_ok(int N, int V, int C, int K) {
   const long tiles_n = N / 256 + 1, tiles_v = V / 256 + 1, tiles_c = C / 256 + 1;
   // the units of a call are numbered in 32 bits: dz, dW, and dx per piece
   return tiles_n * tiles_v < (1L << 28) && tiles_v * tiles_c < (1L << 28) &&
-         tiles_n * tiles_c * (V / kDzMinCols + 1) < (1L << 28);
+         tiles_n * tiles_c * (2 * (V / kDzMinCols) + 1) < (1L << 28);
 }
 
 // K = 0: a single target per row (attn_head_ce), else teacher entries per row.
-HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
+HeadPlan head_plan(int N, int V, int C, int K, bool bwd, bool dw_f32) {
   using namespace head100;
   HeadPlan p;
   size_t off = 0;
@@ -47,9 +50,12 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
   };
   p.rows_pad = (N + kTile - 1) / kTile * kTile;
   long cols = ((long)V + kTile - 1) / kTile * kTile;
+  // rows of lo: with a bf16 dW it is taken where one row tile is kept at most
+  const long lo_pad = !bwd ? 0 : dw_f32 ? p.rows_pad : kTile;
+  p.lo_rows = (int)(lo_pad / 64);
   if (bwd)
-    cols = std::min(cols, std::max((long)(kDzBytes / ((size_t)p.rows_pad * 2)) / kTile * kTile,
-                                   kDzMinCols));
+    cols = std::min(cols, std::max((long)(kDzBytes / ((size_t)(p.rows_pad + lo_pad) * 2)) / kTile * kTile,
+                                   dw_f32 ? kDzMinCols / 2 : kDzMinCols));
   p.pieces = (int)((V + cols - 1) / cols);
   p.piece = (int)(((V + p.pieces - 1) / p.pieces + kTile - 1) / kTile * kTile);
   p.pieces = (V + p.piece - 1) / p.piece;
@@ -82,8 +88,11 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
     p.total = off;
     return p;
   }
-  for (int b = 0; b < std::min(p.pieces, kDzBuffers); ++b)
+  p.lo_blocks = (long)p.lo_rows * (p.piece / kTile);
+  for (int b = 0; b < std::min(p.pieces, kDzBuffers); ++b) {
     p.dz[b] = take((size_t)p.rows_pad * p.piece * 2);
+    p.lo[b] = take((size_t)p.lo_blocks * 64 * kTile * 2);
+  }
   // the accumulators of dx: the most rows that any number of kept rows takes
   const int tn = (C + kTile - 1) / kTile, kb = (std::min(p.piece, V) + kKB - 1) / kKB;
   long rows = p.rows_pad;
@@ -97,6 +106,12 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd) {
   if (K <= kFewNamed) p.rest = take((size_t)N * std::max(K, 1) * 4);
   p.total = off;
   return p;
+}
+
+// The bytes that a call of either type of dW finds enough.
+size_t head_bytes(int N, int V, int C, int K, bool bwd) {
+  const size_t bytes = head_plan(N, V, C, K, bwd, false).total;
+  return bwd ? std::max(bytes, head_plan(N, V, C, K, bwd, true).total) : bytes;
 }
 
 // A matrix [rows][cols] (row pitch `pitch` elements) in boxes of 128 bytes x
@@ -162,7 +177,7 @@ int head_check(const HeadCall& c, void* ws, size_t ws_bytes) {
       !aligned(c.lse_out, 4) || !aligned(c.lse, 4) || !aligned(c.dloss, 4) ||
       !aligned(c.dlse, 4) || !aligned(c.dx, 16) || !aligned(c.dw, 16))
     return ATTN_EALIGN;
-  if (!ws || ws_bytes < head_plan(c.N, c.V, c.C, c.K, c.bwd).total) return ATTN_EWORKSPACE;
+  if (!ws || ws_bytes < head_bytes(c.N, c.V, c.C, c.K, c.bwd)) return ATTN_EWORKSPACE;
   if (!aligned(ws, 16)) return ATTN_EALIGN;
   return ATTN_OK;
 }
@@ -186,7 +201,7 @@ int head_gemm(const head100::Maps& maps, const head100::Params& p, cudaStream_t 
 int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) {
   using namespace head100;
   if (int rc = head_check(c, workspace, ws_bytes)) return rc;
-  const HeadPlan hp = head_plan(c.N, c.V, c.C, c.K, c.bwd);
+  const HeadPlan hp = head_plan(c.N, c.V, c.C, c.K, c.bwd, c.bwd && c.dw_dtype == ATTN_F32);
   cudaStream_t st = (cudaStream_t)stream;
   char* ws = (char*)workspace;
   const int N = c.N, V = c.V, C = c.C, K = c.K;
@@ -283,6 +298,7 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   p.rest = K <= kFewNamed ? (float*)(ws + hp.rest) : nullptr;
   p.dx = (__nv_bfloat16*)c.dx;
   p.dw_f32 = c.dw_dtype == ATTN_F32;
+  p.lo_rows = hp.lo_rows;
   p.c_blocks = C % 64 == 0;
   bool ok = head_map(&maps.dx_out, p.acc, true, hp.acc_rows, C, C, 32) &&
             head_map(&maps.dw_out, c.dw, p.dw_f32 != 0, V, C, C, 32);
@@ -298,6 +314,10 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
     ok = ok && head_map(&maps.dz_k[b], dz, false, hp.rows_pad, hp.piece, hp.piece, 128) &&
          head_block_map(&maps.dz_mn[b], dz, hp.rows_pad, hp.piece) &&
          head_map(&maps.dz_out[b], dz, false, hp.rows_pad, hp.piece, hp.piece, 32);
+    const void* lo = ws + hp.lo[b];
+    ok = ok && head_map(&maps.lo_k[b], lo, false, hp.lo_blocks * 64, kTile, kTile, 128) &&
+         head_block_map(&maps.lo_mn[b], lo, hp.lo_blocks * 64, kTile) &&
+         head_map(&maps.lo_out[b], lo, false, hp.lo_blocks * 64, kTile, kTile, 32);
   }
   if (!ok) return ATTN_ECUDA;
   if (int rc = hp.lw == 128 ? head_gemm<true, 128>(maps, p, st) : head_gemm<true, 256>(maps, p, st))
@@ -315,7 +335,7 @@ extern "C" {
 
 size_t attn_head_workspace_bytes(int N, int V, int C, int K, int is_bwd) {
   if (!head_sizes_ok(N, V, C, K)) return 0;
-  return head_plan(N, V, C, K, is_bwd != 0).total;
+  return head_bytes(N, V, C, K, is_bwd != 0);
 }
 
 int attn_head_ce(const void* x, const void* w, const int32_t* target, float* loss, float* lse,

@@ -20,6 +20,14 @@
 // in fp32, dW of a piece is final. In a row of dx one entry of dz, the target's,
 // outweighs the others: where few ids are named, what their rounding takes is
 // kept and added to dx in fp32, times their rows of W.
+// Where the sums are short or more bits are asked for, dz is carried in two bf16
+// terms, hi + lo (2^-16 relative): lo goes to a buffer of its own, whose K blocks
+// follow hi's in the same accumulator. With an fp32 dW always; and where at most
+// one row tile is kept, since an element of dW then comes from few entries,
+// whose roundings do not average: they took the error of a bf16 dW to twice its
+// output's own rounding (2 rows, 631 ids: 3.8e-3 of dW for 1.7e-3). dx takes
+// lo too where it has no fp32 remainders of named columns. 100 rows of width
+// 768 against 24576 ids take 64 us so, 55 with one term.
 //
 // Rows whose target is absent (or whose upstream gradients are both zero) are
 // left out: the kept rows are compacted first, so the products cost what the
@@ -97,8 +105,9 @@ struct Maps {
   // the row index contiguous (boxes of 64 rows x 64 K, two of them in one box
   // when the extent is a multiple of 64)
   CUtensorMap x_k, xc_k, w_k, x_mn, xc_mn, w_mn, dz_k[kDzBuffers], dz_mn[kDzBuffers];
+  CUtensorMap lo_k[kDzBuffers], lo_mn[kDzBuffers];
   // output boxes of 32 rows x 128 bytes
-  CUtensorMap dz_out[kDzBuffers], dx_out, dw_out;
+  CUtensorMap dz_out[kDzBuffers], lo_out[kDzBuffers], dx_out, dw_out;
 };
 
 // What a kept row brings to its logits' epilogue, by kept row: lse in base 2,
@@ -116,6 +125,7 @@ struct Params {
   int lw;                // columns of a logits tile: 256, or 128 where those are few
   int c_blocks;          // C % 64 == 0: _mn maps of x and W take both 64-wide blocks in one box
   int dw_f32;
+  int lo_rows;           // 64-row blocks per vocabulary tile in lo's buffers
   float inv_tau;
   // null in a forward of one row tile, which takes all rows as they are
   const int* n_kept;     // rows kept (device)
@@ -169,6 +179,8 @@ struct Sched {
   int tm, tc;          // tiles of kept rows, of C
   int kb_c, kb_n;      // K blocks of the logits, of dW
   int splits, kb_per;  // of dx over a whole piece
+  // terms of dz that dW and dx take: 1, or 2, whose K blocks follow the first's
+  int dw_terms, dx_terms;
   bool dx_first;       // the longer units of a group go first
   __host__ __device__ int cols(int p) const { return p + 1 < pieces ? piece : V - p * piece; }
   __host__ __device__ int tv(int p) const { return (cols(p) + kTile - 1) / kTile; }
@@ -192,9 +204,11 @@ __host__ __device__ inline Sched make_sched(const Params& p, int kept) {
   s.kb_c = (p.C + kKB - 1) / kKB;
   s.kb_n = (kept + kKB - 1) / kKB;
   split_dx(s.tm * s.tc, s.kb_v(0), s.splits, s.kb_per);
+  s.dw_terms = p.dw_f32 || kept <= kTile ? 2 : 1;
+  s.dx_terms = p.rest ? 1 : s.dw_terms;
   // split dx units are one per pair and the last to have their dz: they end a
   // group (100 rows, first: 54 us)
-  s.dx_first = s.splits == 1 && s.kb_per > s.kb_n;
+  s.dx_first = s.splits == 1 && s.kb_per * s.dx_terms > s.kb_n * s.dw_terms;
   return s;
 }
 
@@ -253,7 +267,7 @@ __device__ __forceinline__ Unit find_unit(const Sched& s, int u) {
           o.split = u / tiles;
           band_tile(u - o.split * tiles, s.tm, s.tc, kBand, o.tm, o.tn);
           o.kb0 = o.split * s.kb_per;
-          o.nkb = min(s.kb_v(p), o.kb0 + s.kb_per) - o.kb0;
+          o.nkb = (min(s.kb_v(p), o.kb0 + s.kb_per) - o.kb0) * s.dx_terms;
           return o;
         }
         u -= s.dx(p);
@@ -261,7 +275,7 @@ __device__ __forceinline__ Unit find_unit(const Sched& s, int u) {
         if (u < s.dw(p)) {
           o.kind = DW;
           o.p = p;
-          o.nkb = s.kb_n;
+          o.nkb = s.kb_n * s.dw_terms;
           band_tile(u, s.tv(p), s.tc, kBand, o.tm, o.tn);
           return o;
         }
@@ -592,6 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool a_mn = false, b_mn = true, b_one = p.c_blocks != 0;
       const int v0 = un.p * p.piece, buf = un.p % kDzBuffers;
       int bk = 0, brow = un.tn * kTile + rank * 128, bytes = 2 * kStageBytes;
+      int nhi = un.nkb;  // blocks of hi; those of lo follow
       const int arow = un.tm * kTile + rank * 128;
       if (!kBwd || un.kind == DZ) {
         ma = all ? &maps.x_k : &maps.xc_k;
@@ -609,14 +624,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           ma = &maps.dz_k[buf];
           mb = &maps.w_mn;
           bk = v0;
+          nhi /= sc.dx_terms;
         } else {
           ma = &maps.dz_mn[buf];
+          nhi /= sc.dw_terms;
           mb = all ? &maps.x_mn : &maps.xc_mn;
           a_mn = true;
         }
         // dz of its vocabulary tiles: of one (dW), or of its K range
         const int t0 = v0 / kTile + (un.kind == DW ? un.tm : un.kb0 / 4);
-        const int t1 = v0 / kTile + (un.kind == DW ? un.tm : (un.kb0 + un.nkb - 1) / 4);
+        const int t1 = v0 / kTile + (un.kind == DW ? un.tm : (un.kb0 + nhi - 1) / 4);
         if (t0 < dz_from || t1 >= dz_to) {
           ok = wait_tiles(dz_done, t0, t1, v0 / kTile + sc.tv(un.p), sc, lane, dz_to, abort_flag);
           dz_from = t0;
@@ -638,9 +655,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(bar(bFull + s), bytes);
           const uint32_t full = map_rank(bar(bFull + s), 0);
           const uint32_t dst = sb0 + kSmRing + s * kStageBytes;
-          const int k0 = (un.kb0 + kb) * kKB;
-          load_operand(ma, a_mn, true, arow, k0, dst, full);
-          load_operand(mb, b_mn, b_one, brow, bk + k0, dst + kOperandBytes, full);
+          if (!kBwd || kb < nhi) {
+            const int k0 = (un.kb0 + kb) * kKB;
+            load_operand(ma, a_mn, true, arow, k0, dst, full);
+            load_operand(mb, b_mn, b_one, brow, bk + k0, dst + kOperandBytes, full);
+          } else {
+            // block k of the rows (dW) or of the piece's columns (dx) again,
+            // against lo: by vocabulary tile, then by 64 rows, [64][256]
+            const int k = un.kb0 + kb - nhi;
+            if (a_mn) load_operand(&maps.lo_mn[buf], true, true, rank * 128,
+                                   (un.tm * p.lo_rows + k) * 64, dst, full);
+            else load_operand(&maps.lo_k[buf], false, true, (k >> 2) * p.lo_rows * 64 + arow,
+                              (k & 3) * kKB, dst, full);
+            load_operand(mb, b_mn, b_one, brow, bk + k * kKB, dst + kOperandBytes, full);
+          }
         }
         __syncwarp();
         if (++s == kStages) {
@@ -914,6 +942,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (m < kept) p.part[(size_t)(2 * un.tn + half) * p.row_pitch + m] = make_float2(mx, sum);
       } else if (un.kind == DZ) {
         const int buf = un.p % kDzBuffers;
+        // lo goes out beside hi, through the other staging buffer
+        const bool lo = sc.dw_terms == 2;
+        uint32_t even[16];  // lo of the even 32 columns, until the odd ones join
         uint32_t v[2][32];
         tmem_ld32(src, v[0]);
         const float2 k2 = make_float2(c2, c2), l2 = make_float2(-lse2, -lse2),
@@ -984,14 +1015,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_shared_v4(my_row + ((((c & 1) * 4 + e) ^ sw) << 4), pack_bf16(t[8 * e], t[8 * e + 1]),
                          pack_bf16(t[8 * e + 2], t[8 * e + 3]), pack_bf16(t[8 * e + 4], t[8 * e + 5]),
                          pack_bf16(t[8 * e + 6], t[8 * e + 7]));
+          if (lo) {
+            auto left2 = [&](int e) {  // of columns 2 e and 2 e + 1
+              return pack_bf16(t[2 * e] - __bfloat162float(__float2bfloat16_rn(t[2 * e])),
+                               t[2 * e + 1] - __bfloat162float(__float2bfloat16_rn(t[2 * e + 1])));
+            };
+            if ((c & 1) == 0) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) even[e] = left2(e);
+            } else {
+              if (lane == 0) bulk_wait_group_read0();
+              __syncwarp();
+              const uint32_t lo_row = (stage ^ 4096) + lane * 128;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                st_shared_v4(lo_row + ((e ^ sw) << 4), even[4 * e], even[4 * e + 1],
+                             even[4 * e + 2], even[4 * e + 3]);
+                st_shared_v4(lo_row + (((4 + e) ^ sw) << 4), left2(4 * e), left2(4 * e + 1),
+                             left2(4 * e + 2), left2(4 * e + 3));
+              }
+            }
+          }
           if (c & 1) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&maps.dz_out[buf], stage, col0 + 32 * (c - 1), row0);
+              const int at = col0 + 32 * (c - 1);
+              tma_store_2d(&maps.dz_out[buf], stage, at, row0);
               bulk_commit_group();
+              if (lo) {
+                tma_store_2d(&maps.lo_out[buf], stage ^ 4096, at & (kTile - 1),
+                             (at / kTile) * p.lo_rows * 64 + row0);
+                bulk_commit_group();
+              }
             }
-            stage ^= 4096;
+            // the next buffer is the one whose store came first
+            if (!lo) stage ^= 4096;
           }
         }
         if (lane == 0) owed = dz_done + (v0 + un.tn * kLw) / kTile;

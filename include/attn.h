@@ -375,10 +375,13 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
  * and none may overlap an input or the workspace.
  *
  * lse given to the backward is what the forward wrote for the same x, w and
- * temperature. dz is rounded once to bf16, the tensor cores' operand type
- * (2^-8 relative at most, half a step), before its two products: dw carries that rounding
- * in either type. Results do not depend on atomics: the same call gives the
- * same bits.
+ * temperature. dz goes to its two products in bf16, the tensor cores' operand
+ * type. An fp32 dw takes it in two bf16 terms (2^-16 relative at most; a third
+ * more products), and so does a bf16 dw where at most 256 rows are kept; a bf16
+ * dw of more rows takes one term (2^-8, half a step, beside its own rounding).
+ * dx gets back in fp32 what the rounding to one term takes from up to four
+ * named entries; with more of them it takes the terms that dw takes. Results do
+ * not depend on atomics: the same call gives the same bits.
  *
  * Sizes: N, V, C >= 1, C a multiple of 8, K at most 1024; N and V at most
  * 2^26, C at most 2^20 (else ATTN_EUNSUPPORTED). temperature is positive and
@@ -388,8 +391,8 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
  * Workspace: attn_head_workspace_bytes(N, V, C, K, is_bwd) bytes, K = 0 for
  * attn_head_ce*; 0 for invalid sizes. The backward takes the vocabulary in
  * pieces, so its workspace does not grow with V: at most 3 x 96 MiB for dz up
- * to 24576 rows (3 x 4096 bytes a row beyond), plus the kept rows of x and the
- * fp32 sums of dx. (A teacher's lists add at most N (8 K + V / 32) bytes.) Pure
+ * to 24320 rows (3 x 4096 bytes a row beyond), plus the kept rows of x and the
+ * fp32 sums of dx, and is enough for either type of dw. (A teacher's lists add at most N (8 K + V / 32) bytes.) Pure
  * host function.
  */
 size_t attn_head_workspace_bytes(int N, int V, int C, int K, int is_bwd);
