@@ -23,6 +23,9 @@ struct HeadPlan {
   size_t n_kept = 0, ctl = 0, row_of = 0, pos = 0, par = 0, xc = 0, ids = 0, share = 0, entropy = 0, flags = 0, first = 0;
   size_t part = 0, named = 0, exact = 0;  // forward
   size_t dz[head100::kDzBuffers] = {}, lo[head100::kDzBuffers] = {}, acc = 0, rest = 0;  // backward
+  size_t foremost = 0, key = 0, tile_start = 0;
+  int rest_k = 0, tiles = 0;
+  bool keyed = false, sorted = false;
   long acc_rows = 0, lo_blocks = 0;  // of 64 rows x 256 columns, in each of lo's buffers
   int lo_rows = 0;
   int n_ctl = 0, first_pitch = 0;
@@ -50,11 +53,21 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd, bool dw_f32) {
   };
   p.rows_pad = (N + kTile - 1) / kTile * kTile;
   long cols = ((long)V + kTile - 1) / kTile * kTile;
-  // rows of lo: with a bf16 dW it is taken where one row tile is kept at most
+  // The rows' foremost ids matter where a bf16 dW may have more than one row tile
+  // kept; the rows are then sorted by them, while the tiles have room in the
+  // row pass's shared memory.
+  p.keyed = bwd && !dw_f32 && N > kTile;
+  p.tiles = (V + kTile - 1) / kTile;
+  p.sorted = p.keyed && p.tiles <= kMaxSortTiles;
+  // rows of lo in whole: with a bf16 dW where one row tile is kept at most, and
+  // otherwise a staircase of blocks (64 rows x a tile), one row block or one
+  // tile further each
+  const size_t stairs = p.sorted ? (size_t)p.rows_pad / 64 * 64 * kTile * 2 : 0;
   const long lo_pad = !bwd ? 0 : dw_f32 ? p.rows_pad : kTile;
   p.lo_rows = (int)(lo_pad / 64);
   if (bwd)
-    cols = std::min(cols, std::max((long)(kDzBytes / ((size_t)(p.rows_pad + lo_pad) * 2)) / kTile * kTile,
+    cols = std::min(cols, std::max((long)((kDzBytes - std::min(kDzBytes, stairs)) /
+                                           ((size_t)(p.rows_pad + lo_pad) * 2)) / kTile * kTile,
                                    dw_f32 ? kDzMinCols / 2 : kDzMinCols));
   p.pieces = (int)((V + cols - 1) / cols);
   p.piece = (int)(((V + p.pieces - 1) / p.pieces + kTile - 1) / kTile * kTile);
@@ -89,6 +102,7 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd, bool dw_f32) {
     return p;
   }
   p.lo_blocks = (long)p.lo_rows * (p.piece / kTile);
+  if (p.sorted) p.lo_blocks = std::max(p.lo_blocks, (long)p.rows_pad / 64 + p.piece / kTile);
   for (int b = 0; b < std::min(p.pieces, kDzBuffers); ++b) {
     p.dz[b] = take((size_t)p.rows_pad * p.piece * 2);
     p.lo[b] = take((size_t)p.lo_blocks * 64 * kTile * 2);
@@ -103,7 +117,13 @@ HeadPlan head_plan(int N, int V, int C, int K, bool bwd, bool dw_f32) {
   }
   p.acc_rows = rows;
   p.acc = take((size_t)rows * C * 4);
-  if (K <= kFewNamed) p.rest = take((size_t)N * std::max(K, 1) * 4);
+  p.rest_k = K <= kFewNamed ? std::max(K, 1) : p.keyed ? 1 : 0;
+  if (p.rest_k) p.rest = take((size_t)N * p.rest_k * 4);
+  if (p.keyed) {
+    if (K > 0) p.foremost = take((size_t)N * 4);
+    p.key = take((size_t)p.rows_pad * 4);
+  }
+  if (p.sorted) p.tile_start = take((size_t)(p.tiles + 1) * 4);
   p.total = off;
   return p;
 }
@@ -210,6 +230,7 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   float* share = K ? (float*)(ws + hp.share) : nullptr;
   float* entropy = K && !c.bwd ? (float*)(ws + hp.entropy) : nullptr;
   int* flags = K ? (int*)(ws + hp.flags) : nullptr;
+  int* foremost = K && hp.keyed ? (int*)(ws + hp.foremost) : nullptr;
   int *row_of = (int*)(ws + hp.row_of), *pos = (int*)(ws + hp.pos),
       *n_kept = (int*)(ws + hp.n_kept);
   void* xc = ws + hp.xc;
@@ -221,17 +242,21 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
     if (c.t_dtype == ATTN_F32)
       ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_teacher_kernel<float>, blocks, 32 * kTeacherWarps, smem, st,
                                                c.t_idx, (const float*)c.t_logit, inv_tau, c.dloss, c.dlse,
-                                               ids, share, first, hp.first_pitch, hp.lw / 2, entropy, flags, N, V, K));
+                                               ids, share, first, hp.first_pitch, hp.lw / 2, entropy, foremost, flags, N, V, K));
     else
       ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_teacher_kernel<__nv_bfloat16>, blocks, 32 * kTeacherWarps, smem, st,
                                                c.t_idx, (const __nv_bfloat16*)c.t_logit, inv_tau, c.dloss, c.dlse,
-                                               ids, share, first, hp.first_pitch, hp.lw / 2, entropy, flags, N, V, K));
+                                               ids, share, first, hp.first_pitch, hp.lw / 2, entropy, foremost, flags, N, V, K));
   }
   // A forward of one row tile costs the same for any number of kept rows, and
   // its rows do not meet: it goes without the row pass (4 of 27 us at one row).
   const bool whole = !c.bwd && N <= kTile;
   RowsArgs ra = {};
   ra.target = K ? nullptr : c.target;
+  ra.foremost = K ? foremost : c.target;
+  ra.key = hp.keyed ? (int*)(ws + hp.key) : nullptr;
+  ra.tile_start = hp.sorted ? (int*)(ws + hp.tile_start) : nullptr;
+  ra.tiles = hp.tiles;
   ra.flags = flags;
   ra.lse = c.lse;
   ra.dloss = c.dloss;
@@ -252,7 +277,8 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   const int row_blocks = (int)std::min<long>((N + 15L) / 16, 148L);
   ra.rows_per_block = (N + row_blocks - 1) / row_blocks;
   if (!whole)
-    ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_rows_kernel, (unsigned)row_blocks, kRowThreads, 0, st, ra));
+    ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_rows_kernel, (unsigned)row_blocks, kRowThreads,
+                                         hp.sorted ? (size_t)hp.tiles * 8 : 0, st, ra));
   if (launch_status()) return ATTN_ECUDA;
 
   Maps maps = {};
@@ -295,10 +321,13 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
   }
 
   p.acc = (const float*)(ws + hp.acc);
-  p.rest = K <= kFewNamed ? (float*)(ws + hp.rest) : nullptr;
+  p.rest = hp.rest_k ? (float*)(ws + hp.rest) : nullptr;
+  p.rest_k = hp.rest_k;
   p.dx = (__nv_bfloat16*)c.dx;
   p.dw_f32 = c.dw_dtype == ATTN_F32;
   p.lo_rows = hp.lo_rows;
+  p.key = ra.key;
+  p.tile_start = ra.tile_start;
   p.c_blocks = C % 64 == 0;
   bool ok = head_map(&maps.dx_out, p.acc, true, hp.acc_rows, C, C, 32) &&
             head_map(&maps.dw_out, c.dw, p.dw_f32 != 0, V, C, C, 32);
@@ -324,7 +353,8 @@ int head_run(const HeadCall& c, void* workspace, size_t ws_bytes, void* stream) 
     return rc;
   const long n8 = (long)N * (C / 8);
   ATTN_LAUNCH(KK_HEAD_ROWS, st, pdl_launch(head_dx_kernel, (unsigned)std::min<long>((n8 + 255) / 256, 148L * 8),
-                                           256, 0, st, p.acc, row_of, n_kept, p.rest, p.ids, p.w, (uint4*)c.dx,
+                                           256, 0, st, p.acc, row_of, n_kept, p.rest, p.ids,
+                                           K > kFewNamed ? p.key : nullptr, p.w, (uint4*)c.dx,
                                            V, C, p.K, (std::min(hp.piece, V) + kKB - 1) / kKB));
   return launch_status();
 }

@@ -19,13 +19,17 @@ __device__ __forceinline__ bool has_weight(const float* dloss, const float* dlse
 
 // Compacts the kept rows: row_of (kept row -> row), pos (row -> kept row or
 // -1), their number, what each brings to the epilogues (par), and, unless all
-// are kept, their x rows in xc, followed by zero rows up to a multiple of the
-// tile (K values of dz^T x). Order is kept. Every block counts the rows before
+// are kept in order, their x rows in xc, followed by zero rows up to a multiple
+// of the tile (K values of dz^T x). Every block counts the rows before
 // its own from the flags themselves (read from L2, several at a time), so
 // there is one launch and no pass between. Also clears ctl, and dx of the rows
 // left out.
+// Order is kept, or, with tile_start and more than one row tile kept, rows go by
+// the vocabulary tile of their foremost id (a counting sort, stable): the rows
+// that name a tile then are few 64-row blocks, tile_start[t] to tile_start[t + 1].
 // flags: [N] non-zero where the row counts; or null: target in [0, V) and an
 // upstream gradient that is not zero. A target >= V is reported.
+constexpr int kMaxSortTiles = 4096;  // 8 bytes of shared memory each
 struct RowsArgs {
   const int *target, *flags;
   const float *lse, *dloss, *dlse;  // null in the forward (dlse: or when absent)
@@ -33,6 +37,9 @@ struct RowsArgs {
   uint4 *xc, *dx;  // dx: null in the forward
   int *row_of, *pos, *n_kept;
   RowPar* par;
+  const int* foremost;  // by row: the target, or the id of the teacher's largest share
+  int *key, *tile_start;  // foremost by kept row, and [tiles + 1]; or null
+  int tiles;
   unsigned* ctl;
   int n_ctl;
   int N, V, c8, rows_per_block;
@@ -44,25 +51,46 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowsArgs a
   constexpr int kWarps = kRowThreads / 32;
   __shared__ int s_sum[2][kWarps];
   __shared__ int s_warp[kWarps];
+  __shared__ int s_tile[kRowThreads];
+  extern __shared__ int s_count[];  // by tile: kept rows from this block on, then those before
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r0 = blockIdx.x * a.rows_per_block, r1 = min(a.N, r0 + a.rows_per_block);
   for (int i = blockIdx.x * kRowThreads + tid; i < a.n_ctl; i += gridDim.x * kRowThreads)
     a.ctl[i] = 0;
+  const int* __restrict__ foremost = a.foremost;
+  const int* __restrict__ flags = a.flags;
+  const int* __restrict__ target = a.target;
+  const float* __restrict__ dloss = a.dloss;
+  const float* __restrict__ dlse = a.dlse;
   auto counts = [&](int r) -> int {
-    if (a.flags) return a.flags[r] != 0;
-    int k = (unsigned)a.target[r] < (unsigned)a.V;
-    if (a.dloss) {
-      const float g = a.dloss[r], h = a.dlse ? a.dlse[r] : 0.f;
+    if (flags) return flags[r] != 0;
+    int k = (unsigned)target[r] < (unsigned)a.V;
+    if (dloss) {
+      const float g = dloss[r], h = dlse ? dlse[r] : 0.f;
       k &= (g != 0.f) | (h != 0.f);
     }
     return k;
   };
+  if (a.tile_start) {
+    for (int t = tid; t < 2 * a.tiles; t += kRowThreads) s_count[t] = 0;
+    __syncthreads();
+  }
   int before = 0, total = 0;
-#pragma unroll 8
-  for (int r = tid; r < a.N; r += kRowThreads) {
-    const int k = counts(r);
-    total += k;
-    before += r < r0 ? k : 0;
+  for (int b = tid; b < a.N; b += 8 * kRowThreads) {
+    int k[8], f[8];  // eight rows' loads before anything is counted
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = b + j * kRowThreads;
+      k[j] = r < a.N ? counts(r) : 0;
+      f[j] = a.tile_start && r < a.N ? foremost[r] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool earlier = b + j * kRowThreads < r0;
+      total += k[j];
+      before += earlier ? k[j] : 0;
+      if (a.tile_start && k[j]) atomicAdd(&s_count[(earlier ? a.tiles : 0) + f[j] / kTile], 1);
+    }
   }
   for (int o = 16; o > 0; o >>= 1) {
     before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -79,20 +107,60 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowsArgs a
     total += s_sum[1][w];
   }
   if (blockIdx.x == 0 && tid == 0) *a.n_kept = total;
+  const bool sorted = a.tile_start && total > kTile;
+  if (sorted) {
+    // where each tile's rows start, and this block's among them: a few tiles a thread
+    const int each = (a.tiles + kRowThreads - 1) / kRowThreads;
+    const int t0 = min(a.tiles, tid * each), t1 = min(a.tiles, t0 + each);
+    int sum = 0;
+    for (int t = t0; t < t1; ++t) sum += s_count[t] + s_count[a.tiles + t];
+    int upto = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int below = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += below;
+    }
+    if (lane == 31) s_warp[warp] = upto;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) upto += s_warp[w];
+    int start = upto - sum;
+    for (int t = t0; t < t1; ++t) {
+      const int own = s_count[t], earlier = s_count[a.tiles + t];
+      if (blockIdx.x == 0) a.tile_start[t] = start;
+      s_count[t] = start + earlier;
+      start += own + earlier;
+    }
+    if (blockIdx.x == 0 && tid == 0) a.tile_start[a.tiles] = total;
+    __syncthreads();
+  }
   for (int b = r0; b < r1; b += kRowThreads) {
     const int r = b + tid;
     const bool in = r < r1;
     const bool k = in && counts(r);
     if (in && a.target && a.target[r] >= a.V) report_status(ATTN_EDEVICE_INPUT);
-    const unsigned votes = __ballot_sync(0xffffffffu, k);
-    if (lane == 0) s_warp[warp] = __popc(votes);
-    __syncthreads();
-    int at = before, all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      at += w < warp ? s_warp[w] : 0;
-      all += s_warp[w];
+    int at = 0;
+    if (sorted) {
+      const int t = k ? foremost[r] / kTile : -1;
+      s_tile[tid] = t;
+      __syncthreads();
+      if (k) {
+        at = s_count[t];
+        for (int i = 0; i < tid; ++i) at += s_tile[i] == t ? 1 : 0;
+      }
+      __syncthreads();
+      if (k) atomicAdd(&s_count[t], 1);
+    } else {
+      const unsigned votes = __ballot_sync(0xffffffffu, k);
+      if (lane == 0) s_warp[warp] = __popc(votes);
+      __syncthreads();
+      int all = 0;
+      at = before;
+      for (int w = 0; w < kWarps; ++w) {
+        at += w < warp ? s_warp[w] : 0;
+        all += s_warp[w];
+      }
+      at += __popc(votes & ((1u << lane) - 1u));
+      before += all;
     }
-    at += __popc(votes & ((1u << lane) - 1u));
     if (in) a.pos[r] = k ? at : -1;
     if (k) {
       a.row_of[at] = r;
@@ -104,22 +172,30 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowsArgs a
         rp.cb = g * a.inv_tau;
       }
       a.par[at] = rp;
+      if (a.key) a.key[at] = foremost[r];
     }
-    before += all;
     __syncthreads();
   }
-  if (total == a.N) return;  // the products read x in place
-  // a warp copies a row at a time (its pos entries were written by this block)
+  if (total == a.N && !sorted) return;  // the products read x in place
+  // a warp copies four rows at a time (their pos entries were written by this block)
   const uint4* __restrict__ x = a.x;
   uint4* __restrict__ xc = a.xc;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int r = r0 + warp; r < r1; r += kWarps) {
-    const int at = a.pos[r];
-    if (at >= 0) {
-#pragma unroll 4
-      for (int i = lane; i < a.c8; i += 32) xc[(size_t)at * a.c8 + i] = x[(size_t)r * a.c8 + i];
-    } else if (a.dx) {
-      for (int i = lane; i < a.c8; i += 32) a.dx[(size_t)r * a.c8 + i] = zero;
+  for (int r = r0 + warp; r < r1; r += 4 * kWarps) {
+    int at[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) at[j] = r + j * kWarps < r1 ? a.pos[r + j * kWarps] : -2;
+#pragma unroll 2
+    for (int i = lane; i < a.c8; i += 32) {
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = at[j] >= 0 ? x[(size_t)(r + j * kWarps) * a.c8 + i] : zero;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (at[j] >= 0) xc[(size_t)at[j] * a.c8 + i] = v[j];
+        else if (at[j] == -1 && a.dx) a.dx[(size_t)(r + j * kWarps) * a.c8 + i] = zero;
+      }
     }
   }
   const int pad = slot_rows(total);
@@ -130,7 +206,8 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowsArgs a
 // The teacher's list of one row per warp: q = softmax of t / tau over the
 // entries present (0 <= id < V), ids sorted ascending with their q (absent
 // ones last, id INT_MAX, q 0), how many of them lie below each multiple of
-// first_cols columns, sum q log q, and whether the row counts (some entry above -inf, and
+// first_cols columns, sum q log q, the id of the largest share (the lowest such
+// id), and whether the row counts (some entry above -inf, and
 // an upstream gradient that is not zero). The sort is by rank (K comparisons
 // per entry): stable, so equal ids keep their order. The maximum is taken off
 // before the division by tau: entries at the type's lowest value then differ
@@ -141,7 +218,8 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
                         float inv_tau, const float* __restrict__ dloss,
                         const float* __restrict__ dlse, int* __restrict__ ids,
                         float* __restrict__ share, uint16_t* __restrict__ first, int first_pitch, int first_cols,
-                        float* __restrict__ entropy, int* __restrict__ flags, int N, int V, int K) {
+                        float* __restrict__ entropy, int* __restrict__ foremost,
+                        int* __restrict__ flags, int N, int V, int K) {
   pdl_wait_and_trigger();
   extern __shared__ __align__(16) int smem_teacher[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -208,6 +286,13 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
         else hi = mid;
       }
       first[(size_t)r * first_pitch + b] = (uint16_t)lo;
+    }
+    if (foremost) {
+      int id = INT_MAX;
+      for (int k = lane; k < K; k += 32)
+        if (key[k] < id && (nan || to_f32(tl[k]) == top)) id = key[k];
+      id = __reduce_min_sync(0xffffffffu, id);
+      if (lane == 0) foremost[r] = id;
     }
     if (lane == 0) {
       flags[r] = some && has_weight(dloss, dlse, r) ? 1 : 0;
@@ -311,19 +396,24 @@ __global__ void __launch_bounds__(kLossThreads)
 }
 
 // dx of the kept rows where its vocabulary axis was split: the accumulators
-// added in order, then what the rounding of dz took from the named columns, and
-// rounded once. Eight columns per thread. Without a split
+// added in order, then what the rounding of dz took from the named columns (key
+// instead of ids: from the foremost one), and rounded once. Eight columns per thread. Without a split
 // the last piece's epilogue has written dx, and this pass ends at once.
 __global__ void __launch_bounds__(256)
     head_dx_kernel(const float* __restrict__ acc, const int* __restrict__ row_of,
                    const int* __restrict__ n_kept, const float* __restrict__ rest,
-                   const int* __restrict__ ids, const uint4* __restrict__ w,
-                   uint4* __restrict__ dx, int V, int C, int K, int kb_total) {
+                   const int* __restrict__ ids, const int* __restrict__ key,
+                   const uint4* __restrict__ w, uint4* __restrict__ dx, int V, int C, int K,
+                   int kb_total) {
   pdl_wait_and_trigger();
   const int kept = *n_kept;
   int splits, kb_per;
   split_dx(((kept + kTile - 1) / kTile) * ((C + kTile - 1) / kTile), kb_total, splits, kb_per);
   if (splits == 1) return;
+  if (key) {
+    K = 1;
+    if (kept <= kTile) rest = nullptr;  // both terms of dz were multiplied
+  }
   const size_t slot = (size_t)slot_rows(kept) * C;
   const int c8 = C / 8;
   const long n = (long)kept * c8;
@@ -338,7 +428,7 @@ __global__ void __launch_bounds__(256)
       g[k] = 0.f;
       wv[k] = make_uint4(0, 0, 0, 0);
       if (rest && k < K) {
-        const int id = ids[(size_t)row * K + k];
+        const int id = key ? key[m] : ids[(size_t)row * K + k];
         if ((unsigned)id < (unsigned)V) {
           g[k] = rest[(size_t)m * K + k];
           wv[k] = w[(size_t)id * c8 + c / 8];

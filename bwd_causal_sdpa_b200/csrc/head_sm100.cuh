@@ -27,7 +27,16 @@
 // whose roundings do not average: they took the error of a bf16 dW to twice its
 // output's own rounding (2 rows, 631 ids: 3.8e-3 of dW for 1.7e-3). dx takes
 // lo too where it has no fp32 remainders of named columns. 100 rows of width
-// 768 against 24576 ids take 64 us so, 55 with one term.
+// 768 against 24576 ids take 61 us so, 55 with one term.
+// A bf16 dW of more rows takes lo where a row names its foremost id (the target,
+// or a teacher's largest share): that entry outweighs its row, and when every
+// row's dloss is the same, as in a mean, all of them round alike and the error
+// is one factor, up to 2^-8, on their part of dW. The row pass sorts the kept
+// rows by the vocabulary tile of that id, so blocks of 64 rows meet the tiles
+// they name along a staircase: at most (rows / 64 + tiles) blocks of lo exist,
+// of rows / 64 x tiles, and they are all that is stored and multiplied. 8192
+// rows of width 768: 0.99 of 0.97 ms, with the sort and the gather of x; all of
+// lo would take a third more.
 //
 // Rows whose target is absent (or whose upstream gradients are both zero) are
 // left out: the kept rows are compacted first, so the products cost what the
@@ -126,6 +135,8 @@ struct Params {
   int c_blocks;          // C % 64 == 0: _mn maps of x and W take both 64-wide blocks in one box
   int dw_f32;
   int lo_rows;           // 64-row blocks per vocabulary tile in lo's buffers
+  const int* key;        // by kept row: the id of its foremost entry, or null
+  const int* tile_start; // rows go by key: the first of each vocabulary tile; or null
   float inv_tau;
   // null in a forward of one row tile, which takes all rows as they are
   const int* n_kept;     // rows kept (device)
@@ -140,8 +151,10 @@ struct Params {
   float* exact;          // the same from plain fp32 sums, for few ids per row, or null
   int row_pitch;
   // what rounding dz to bf16 takes from the row's named columns, by kept row,
-  // where they are few: dx gets it back times their rows of W (or null)
+  // where they are few, or from its foremost one (rest_k of them a row): dx gets
+  // it back times their rows of W (or null)
   float* rest;
+  int rest_k;
   const float* acc;      // fp32 sums of dx, slot_rows(kept) rows per split
   __nv_bfloat16* dx;
   // zero at launch: [0] the next unit; then counters, in epilogue warps: per
@@ -181,6 +194,8 @@ struct Sched {
   int splits, kb_per;  // of dx over a whole piece
   // terms of dz that dW and dx take: 1, or 2, whose K blocks follow the first's
   int dw_terms, dx_terms;
+  const int* tile_start;  // null where rows are in order
+  int lo_step;            // 64-row blocks of lo between one vocabulary tile and the next
   bool dx_first;       // the longer units of a group go first
   __host__ __device__ int cols(int p) const { return p + 1 < pieces ? piece : V - p * piece; }
   __host__ __device__ int tv(int p) const { return (cols(p) + kTile - 1) / kTile; }
@@ -205,7 +220,9 @@ __host__ __device__ inline Sched make_sched(const Params& p, int kept) {
   s.kb_n = (kept + kKB - 1) / kKB;
   split_dx(s.tm * s.tc, s.kb_v(0), s.splits, s.kb_per);
   s.dw_terms = p.dw_f32 || kept <= kTile ? 2 : 1;
-  s.dx_terms = p.rest ? 1 : s.dw_terms;
+  s.dx_terms = p.K <= kFewNamed ? 1 : s.dw_terms;
+  s.tile_start = s.dw_terms == 1 ? p.tile_start : nullptr;
+  s.lo_step = s.tile_start ? 1 : p.lo_rows;
   // split dx units are one per pair and the last to have their dz: they end a
   // group (100 rows, first: 54 us)
   s.dx_first = s.splits == 1 && s.kb_per * s.dx_terms > s.kb_n * s.dw_terms;
@@ -277,6 +294,14 @@ __device__ __forceinline__ Unit find_unit(const Sched& s, int u) {
           o.p = p;
           o.nkb = s.kb_n * s.dw_terms;
           band_tile(u, s.tv(p), s.tc, kBand, o.tm, o.tn);
+          if (s.tile_start) {  // lo of the rows that name this tile
+            const int* at = s.tile_start + p * (s.piece / kTile) + o.tm;
+            const int r0 = at[0], r1 = at[1];
+            if (r0 < r1) {
+              o.kb0 = r0 / kKB;
+              o.nkb += (r1 + kKB - 1) / kKB - o.kb0;
+            }
+          }
           return o;
         }
         u -= s.dw(p);
@@ -594,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ---------------- TMA ----------------
     const bool el = elect_one();
-    const bool all = kept == p.N;  // every row kept: x is read in place
+    const bool all = kept == p.N && !sc.tile_start;  // x is read in place
     int s = 0;
     uint32_t phase = 1;  // a fresh barrier's previous phase counts as complete
     int used_ok = -1, dx_ok = -1;  // pieces whose counters are known to be full
@@ -627,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           nhi /= sc.dx_terms;
         } else {
           ma = &maps.dz_mn[buf];
-          nhi /= sc.dw_terms;
+          nhi = sc.kb_n;
           mb = all ? &maps.x_mn : &maps.xc_mn;
           a_mn = true;
         }
@@ -656,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t full = map_rank(bar(bFull + s), 0);
           const uint32_t dst = sb0 + kSmRing + s * kStageBytes;
           if (!kBwd || kb < nhi) {
-            const int k0 = (un.kb0 + kb) * kKB;
+            const int k0 = ((a_mn ? 0 : un.kb0) + kb) * kKB;
             load_operand(ma, a_mn, true, arow, k0, dst, full);
             load_operand(mb, b_mn, b_one, brow, bk + k0, dst + kOperandBytes, full);
           } else {
@@ -664,8 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // against lo: by vocabulary tile, then by 64 rows, [64][256]
             const int k = un.kb0 + kb - nhi;
             if (a_mn) load_operand(&maps.lo_mn[buf], true, true, rank * 128,
-                                   (un.tm * p.lo_rows + k) * 64, dst, full);
-            else load_operand(&maps.lo_k[buf], false, true, (k >> 2) * p.lo_rows * 64 + arow,
+                                   (un.tm * sc.lo_step + k) * 64, dst, full);
+            else load_operand(&maps.lo_k[buf], false, true, (k >> 2) * sc.lo_step * 64 + arow,
                               (k & 3) * kKB, dst, full);
             load_operand(mb, b_mn, b_one, brow, bk + k * kKB, dst + kOperandBytes, full);
           }
@@ -824,8 +849,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // what the unit's row needs, fetched while the unit before is worked on
     RowPar rp = {0.f, 0.f, 0.f, 0};
     int n_from = 0, n_to = 0;
+    int key = -1, key2 = -1;  // foremost ids of this row and of one in the other half of its 64
     auto fetch_row = [&](const Unit& w) {
       const int m = w.tm * kTile + rank * 128 + sub * 32 + lane;
+      if (kBwd && p.key && w.kind == DZ) {
+        key = m < kept ? p.key[m] : -1;
+        key2 = (m ^ 32) < kept ? p.key[m ^ 32] : -1;
+      }
       if (!kBwd && !p.n_kept) rp.id = m < kept && !p.share ? p.ids[m] : m;
       else if (w.kind <= DZ && m < kept) rp = p.par[m];
     };
@@ -857,6 +887,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.share && n_from < n_to)
         nm.list(p.ids + (size_t)rp.id * p.K, p.share + (size_t)rp.id * p.K, n_from, n_to);
       const float lse2 = rp.lse2, ca = rp.ca, cb = rp.cb;
+      // lo of this unit: all of it, or where a row of the 64 names the unit's tile
+      const int vtile = (v0 + un.tn * kLw) / kTile, row_key = key;
+      const bool unit_lo =
+          kBwd && (sc.dw_terms == 2 ||
+                   (sc.tile_start && __any_sync(0xffffffffu, key >= 0 && key / kTile == vtile ||
+                                                                 key2 >= 0 && key2 / kTile == vtile)));
       // without a list: within these columns or not
       const int target = m < kept ? rp.id - (v0 + col0) : -1;
       const uint32_t full = bar(bAccFull + a), par = (n >> 1) & 1;
@@ -943,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (un.kind == DZ) {
         const int buf = un.p % kDzBuffers;
         // lo goes out beside hi, through the other staging buffer
-        const bool lo = sc.dw_terms == 2;
+        const bool lo = unit_lo;
         uint32_t even[16];  // lo of the even 32 columns, until the odd ones join
         uint32_t v[2][32];
         tmem_ld32(src, v[0]);
@@ -981,9 +1017,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t at = mine + (((e >> 2) ^ sw) << 4) + (e & 3) * 4;
                 const float d = fmaf(-cb, nm.share[0], ld_shared_f32(at));
                 st_shared_f32(at, d);
-                if (p.rest)  // of an id named again, the last one's counts
-                  p.rest[(size_t)m * p.K + nm.pos] =
-                      nm.id[1] == nm.id[0] ? 0.f : d - __bfloat162float(__float2bfloat16_rn(d));
+                if (p.rest) {  // of an id named again, the last one's counts
+                  const float r = d - __bfloat162float(__float2bfloat16_rn(d));
+                  if (p.rest_k == p.K) p.rest[(size_t)m * p.K + nm.pos] = nm.id[1] == nm.id[0] ? 0.f : r;
+                  else if (nm.id[0] == row_key) p.rest[m] = r;
+                }
                 nm.advance();
               }
 #pragma unroll
@@ -1045,7 +1083,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               bulk_commit_group();
               if (lo) {
                 tma_store_2d(&maps.lo_out[buf], stage ^ 4096, at & (kTile - 1),
-                             (at / kTile) * p.lo_rows * 64 + row0);
+                             (at / kTile) * sc.lo_step * 64 + row0);
                 bulk_commit_group();
               }
             }
@@ -1078,15 +1116,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = m < kept ? p.row_of[m] : 0;
           float rest[kFewNamed];
           int id[kFewNamed];
+          const int n_rest = p.rest && sc.dx_terms == 1 ? p.rest_k : 0;
 #pragma unroll
           for (int k = 0; k < kFewNamed; ++k) {
             rest[k] = 0.f;
             id[k] = 0;
-            if (p.rest && k < p.K && m < kept) {
-              const int named = p.ids[(size_t)row * p.K + k];
+            if (n_rest > k && m < kept) {
+              const int named = p.rest_k == p.K ? p.ids[(size_t)row * p.K + k] : p.key[m];
               if ((unsigned)named < (unsigned)p.V) {
                 id[k] = named;
-                rest[k] = __ldcg(p.rest + (size_t)m * p.K + k);
+                rest[k] = __ldcg(p.rest + (size_t)m * p.rest_k + k);
               }
             }
           }
@@ -1104,7 +1143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int k = 0; k < kFewNamed; ++k) {
-              if (!p.rest || k >= p.K) break;
+              if (k >= n_rest) break;
               uint2 wv[8];  // rows of W (row 0 where there is nothing to add): all on their way
 #pragma unroll
               for (int i = 0; i < 8; ++i) {

@@ -376,12 +376,16 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
  *
  * lse given to the backward is what the forward wrote for the same x, w and
  * temperature. dz goes to its two products in bf16, the tensor cores' operand
- * type. An fp32 dw takes it in two bf16 terms (2^-16 relative at most; a third
- * more products), and so does a bf16 dw where at most 256 rows are kept; a bf16
- * dw of more rows takes one term (2^-8, half a step, beside its own rounding).
- * dx gets back in fp32 what the rounding to one term takes from up to four
- * named entries; with more of them it takes the terms that dw takes. Results do
- * not depend on atomics: the same call gives the same bits.
+ * type: in one term (2^-8 relative at most, half a step, beside the output's own
+ * rounding) or in two (2^-16).
+ *   dw: two terms in fp32 (a third more products), and in bf16 where at most 256
+ *       rows are kept; with more of them two terms for the foremost entry of a
+ *       row (its target, or the teacher's largest share, the lowest such id),
+ *       the one that outweighs the others (V at most 2^20, else one term);
+ *   dx: one term, and in fp32 what the rounding takes from up to four named
+ *       entries; where the teacher has more, two terms as in dw, or what the
+ *       rounding takes from the foremost one.
+ * Results do not depend on atomics: the same call gives the same bits.
  *
  * Sizes: N, V, C >= 1, C a multiple of 8, K at most 1024; N and V at most
  * 2^26, C at most 2^20 (else ATTN_EUNSUPPORTED). temperature is positive and
@@ -391,7 +395,7 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
  * Workspace: attn_head_workspace_bytes(N, V, C, K, is_bwd) bytes, K = 0 for
  * attn_head_ce*; 0 for invalid sizes. The backward takes the vocabulary in
  * pieces, so its workspace does not grow with V: at most 3 x 96 MiB for dz up
- * to 24320 rows (3 x 4096 bytes a row beyond), plus the kept rows of x and the
+ * to 21504 rows (3 x 4608 bytes a row beyond, and 1 MiB), plus the kept rows of x and the
  * fp32 sums of dx, and is enough for either type of dw. (A teacher's lists add at most N (8 K + V / 32) bytes.) Pure
  * host function.
  */

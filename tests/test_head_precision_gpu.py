@@ -3,8 +3,10 @@
 dz is the tensor cores' operand, in bf16 (half a step: 2^-8 relative). In two
 terms, hi + lo, both bf16, what is left of an entry is half a step of lo:
 2^-8 2^-8 = 2^-16. The library states where it takes two: for an fp32 dW, and
-where at most 256 rows are kept; and dx gets what the rounding takes from up to
-four named entries in fp32. Bounds, element by element, as in test_head_gpu.py with that
+where at most 256 rows are kept; for a bf16 dW of more rows at the foremost
+entry of each (the target, or a teacher's largest share); and dx gets what the
+rounding takes from up to four named entries, of more of them from the foremost
+one, in fp32. Bounds, element by element, as in test_head_gpu.py with that
 half step in its place:
 
   D = b |dz| + (2 e + 2^-20) |a| p + 2^-20 |g| q,   b = 2^-16 or 2^-8,
@@ -25,17 +27,22 @@ pytestmark = pytest.mark.gpu
 
 
 def _named(ids, q, V):
+    """Shares over the vocabulary, and where the named and the foremost ids are."""
+    rows = np.arange(ids.shape[0])
     share = np.zeros((ids.shape[0], V))
-    rows = np.broadcast_to(np.arange(ids.shape[0])[:, None], ids.shape)
-    np.add.at(share, (rows, np.maximum(ids, 0)), np.where(ids >= 0, q, 0.0))
-    mark = np.zeros(share.shape, bool)
-    mark[rows[ids >= 0], ids[ids >= 0]] = True
-    return share, mark
+    named, foremost = np.zeros(share.shape, bool), np.zeros(share.shape, bool)
+    here = ids >= 0
+    at = np.broadcast_to(rows[:, None], ids.shape)
+    np.add.at(share, (at, np.maximum(ids, 0)), np.where(here, q, 0.0))
+    named[at[here], ids[here]] = True
+    top = np.where(here, q, -1.0).argmax(axis=1)
+    some = here.any(axis=1)
+    foremost[rows[some], ids[rows, top][some]] = True
+    return share, named, foremost
 
 
-def _check(w, dw_f32, dx_all, dw_all, dw_named=False):
-    """dx_all, dw_all: two terms everywhere; else at the named entries of dx
-    with up to four of them, and of dW with dw_named."""
+def _check(w, dw_f32, all_terms):
+    """all_terms: at most 256 rows are kept."""
     from bwd_causal_sdpa_b200 import ATTN_BF16, ATTN_F32, ATTN_OK
     from bwd_causal_sdpa_b200.runner import HeadRunner
 
@@ -47,29 +54,31 @@ def _check(w, dw_f32, dx_all, dw_all, dw_named=False):
     got = r.results()
     ids, q = teacher_lists(w.t_idx, w.t_logit, c.V, c.tau) if c.K else target_lists(w.target, c.V)
     kept = (ids >= 0).any(axis=1)
+    assert all_terms == (kept.sum() <= 256)
     x, W = w.x.astype(np.float64), w.w.astype(np.float64)
     x[~kept] = 0.0
     _, lse = head_loss(x, W, ids, q, c.tau)
     dz = np.abs(head_dz(x, W, ids, q, w.dloss, w.dlse, c.tau))
     dx, dw = head_loss_backward(x, W, ids, q, w.dloss, w.dlse, c.tau)
-    share, mark = _named(ids, q, c.V)
+    share, named, foremost = _named(ids, q, c.V)
     S = (np.abs(x) @ np.abs(W).T / c.tau).max(axis=1)
     e = (c.C / 16 + 2) * 2.0**-23 * S + 2.0**-20 * (1 + np.abs(lse))
     p = np.exp(x @ W.T / c.tau - lse[:, None]) * kept[:, None]
     a = np.abs(w.dloss.astype(np.float64) + w.dlse) / c.tau
     slack = (2 * e + 2.0**-20)[:, None] * a[:, None] * p
     slack += 2.0**-20 * share * np.abs(w.dloss)[:, None] / c.tau
-    fine = lambda everywhere, named: np.where(mark & named | everywhere, 2.0**-16, 2.0**-8)  # noqa: E731
+    two = all_terms or dw_f32
+    b_dw = np.where(two | foremost, 2.0**-16, 2.0**-8)
+    b_dx = np.where(named if c.K <= 4 else two | foremost, 2.0**-16, 2.0**-8)
     total = lambda n: (n / 8 + 10) * 2.0**-23  # noqa: E731
-    D = (fine(dx_all, c.K <= 4) + total(c.V)) * dz + slack
-    b_dx = D @ np.abs(W) + 2.0**-8 * np.abs(dx)
-    D = (fine(dw_all, dw_named) + total(c.N)) * dz + slack
-    b_dw = D.T @ np.abs(x) + (0.0 if dw_f32 else 2.0**-8) * np.abs(dw)
+    b_dx = ((b_dx + total(c.V)) * dz + slack) @ np.abs(W) + 2.0**-8 * np.abs(dx)
+    b_dw = ((b_dw + total(c.N)) * dz + slack).T @ np.abs(x)
+    b_dw += (0.0 if dw_f32 else 2.0**-8) * np.abs(dw)
     for name, ref, bound in (("dx", dx, b_dx), ("dw", dw, b_dw)):
         off = np.abs(got[name] - ref)
         bad = ~(off <= bound + 1e-37)  # fp32 results below the normal range are flushed
         assert not bad.any(), (name, c, int(bad.sum()), np.argwhere(bad)[:3].tolist(),
-                               (off / bound)[bad].max())
+                               (off / np.maximum(bound, 1e-37))[bad].max())
 
 
 CONFIG = {0: "head_small", 1: "head_distill_small"}
@@ -87,12 +96,18 @@ def _workload(N, K, **kw):
 @pytest.mark.parametrize("K", [0, 3, 40])
 @pytest.mark.parametrize("N", [1, 70, 300, 700])
 def test_fp32_dw_holds_two_terms(N, K):
-    # dx takes its named entries from the fp32 remainders, or both terms as dW
-    _check(_workload(N, K), True, K > 4, True)
+    _check(_workload(N, K), True, N <= 256)
 
 
 @pytest.mark.parametrize("K", [0, 2, 4, 5, 40])
 @pytest.mark.parametrize("N,left_out", [(1, 0.0), (2, 0.0), (9, 0.5), (40, 0.0), (200, 0.1),
                                         (256, 0.0), (800, 0.7)])
 def test_few_rows_hold_two_terms(N, left_out, K):
-    _check(_workload(N, K, left_out=left_out), False, K > 4, True)
+    _check(_workload(N, K, left_out=left_out), False, True)
+
+
+@pytest.mark.parametrize("K", [0, 1, 3, 30])
+@pytest.mark.parametrize("N,V,C,left_out", [(257, 5000, 72, 0.0), (700, 6000, 72, 0.0),
+                                            (1100, 3001, 200, 0.3), (1500, 130, 64, 0.0)])
+def test_foremost_entries_of_many_rows_hold_two_terms(N, V, C, left_out, K):
+    _check(_workload(N, K, V=V, C=C, left_out=left_out), False, False)
