@@ -98,8 +98,9 @@ constexpr int kSmRing = 0;
 constexpr int kSmStage = kStages * kStageBytes;          // 2 x 4 KB per epilogue warp
 constexpr int kSmBars = kSmStage + kEpiWarps * 8192;
 constexpr int bFull = 0, bEmpty = kStages, bAccFull = 2 * kStages, bAccEmpty = 2 * kStages + 2,
-              bTkFull = 2 * kStages + 4, bTkEmpty = bTkFull + kTickets, bWant = bTkEmpty + kTickets;
-constexpr int kNumBars = bWant + 2;  // (one to keep what follows 16-byte aligned)
+              bTkFull = 2 * kStages + 4, bTkEmpty = bTkFull + kTickets, bWant = bTkEmpty + kTickets,
+              bTkRead = bWant + 1;
+constexpr int kNumBars = (bTkRead + kTickets + 1) / 2 * 2;  // what follows is 16-byte aligned
 constexpr int kSmTickets = kSmBars + kNumBars * 8;       // kTickets x 32 bytes
 constexpr int kSmMisc = kSmTickets + kTickets * 32;
 constexpr int kSmAlloc = kSmMisc + 16;
@@ -361,11 +362,10 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t a, int x, int y, int z, i
                "r"(w)
                : "memory");
 }
-// Arrive on a barrier of either CTA (an address of map_rank) for reads that are
-// done: no release at cluster scope, which first waits for all that the warp
-// has in flight (2800 cycles per unit in the MMA warp, whose products drained).
-__device__ __forceinline__ void mbar_arrive_read(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Arrive for reads of tensor memory that tcgen05.wait::ld and
+// tcgen05.fence::before_thread_sync have closed: nothing else hangs on it.
+__device__ __forceinline__ void mbar_arrive_tmem(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -563,8 +563,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < kTickets; ++t) {
       mbar_init(bar(bTkFull + t), 1);
-      // readers: the epilogue and TMA warps of both CTAs, CTA 0's MMA warp
-      mbar_init(bar(bTkEmpty + t), 2 * kEpiWarps + 3);
+      // readers: CTA 0's epilogue, TMA and MMA warps, and for those of CTA 1,
+      // which arrive on its bTkRead, one that passes it on
+      mbar_init(bar(bTkEmpty + t), kEpiWarps + 3);
+      mbar_init(bar(bTkRead + t), kEpiWarps + 1);
     }
     mbar_init(bar(bWant), 1);
     *abort_flag = 0;
@@ -605,7 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     un.kb0 = b.y;
     un.nkb = b.z;
     const bool more = __any_sync(0xffffffffu, un.kind != END);  // every lane has its values
-    if (lane == 0) mbar_arrive_read(map_rank(bar(bTkEmpty + t), 0));
+    if (lane == 0) mbar_arrive(bar((rank == 0 ? bTkEmpty : bTkRead) + t));
+    __syncwarp();
     return more;
   };
   unsigned* const dz_used = p.ctl + kCtlPieces;
@@ -751,6 +754,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (el) commit_pair(bar(bAccFull + a));
         __syncwarp();
         ok = next_unit(n + 1, un);
+      }
+    } else if (kBwd) {
+      // CTA 1's tickets are written by CTA 0, so their reads have to be released
+      // at cluster scope. That waits for all that a warp has in flight (2 to 5 %
+      // of the backward when the readers do it, 2800 cycles per unit in a warp
+      // that issues products): this idle warp does it for them.
+      for (int n = 0;; ++n) {
+        const int t = n % kTickets;
+        if (!warp_wait_cl(bar(bTkFull + t), (n / kTickets) & 1, abort_flag)) break;
+        const int kind = *reinterpret_cast<const int*>(smem_raw + kSmTickets + t * 32);
+        if (__any_sync(0xffffffffu, kind == END)) break;
+        if (!warp_wait(bar(bTkRead + t), (n / kTickets) & 1, abort_flag)) break;
+        if (lane == 0) mbar_arrive_remote(map_rank(bar(bTkEmpty + t), 0));
+        __syncwarp();
       }
     }
   } else if (kBwd && warp == 2 + kEpiWarps) {
@@ -904,11 +921,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       Unit nu;
       more = next_unit(n + 1, nu);
       if (more) fetch_row(nu);
+      __syncwarp();  // tcgen05.ld and its wait take a converged warp, here and below
       auto release = [&]() {
         // every column of this accumulator that this warp uses has been read
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_read(map_rank(bar(bAccEmpty + a), 0));
+        if (lane == 0) mbar_arrive_tmem(map_rank(bar(bAccEmpty + a), 0));
+        __syncwarp();
       };
       const uint32_t src = tl + a * kTile + half * (logits ? lhalf : 128);
       if constexpr (!kBwd) {
@@ -974,6 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) sum += f[e] == -INFINITY ? 0.f : f[e];
           }
+          __syncwarp();
         }
         if (m < kept) p.part[(size_t)(2 * un.tn + half) * p.row_pitch + m] = make_float2(mx, sum);
       } else if (un.kind == DZ) {
@@ -1090,6 +1110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the next buffer is the one whose store came first
             if (!lo) stage ^= 4096;
           }
+          __syncwarp();
         }
         if (lane == 0) owed = dz_done + (v0 + un.tn * kLw) / kTile;
       } else {
@@ -1157,6 +1178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (g != 0.f) add_scaled4(sum[i], g, wv[i]);
               }
             }
+            __syncwarp();
             uint32_t v[32];
             tmem_ld32(src + 32 * c, v);
             tmem_wait_ld();
@@ -1188,6 +1210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int cs = col0 + 32 * c;
+          __syncwarp();
           tmem_wait_ld();
           if (c < 3) tmem_ld32(src + 32 * (c + 1), vv[(c + 1) & 1]);
           else release();
@@ -1235,6 +1258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before();
+  __syncwarp();
   __syncthreads();
   cluster_sync_all();  // no CTA leaves (or frees TMEM) while the other may still signal it
   if (warp == 1) {
