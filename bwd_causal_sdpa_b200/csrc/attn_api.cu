@@ -767,7 +767,7 @@ int attn_exp2_selftest(const float* x, float* y, int n, void* stream) {
 
 int attn_debug_withhold(int what) {
 #ifdef ATTN_DEBUG_HOOKS
-  if (what < 0 || what > 1) return ATTN_EINVAL;
+  if (what < 0 || what > 3) return ATTN_EINVAL;
   return cudaMemcpyToSymbol(g_attn_withhold, &what, sizeof(int)) == cudaSuccess ? ATTN_OK
                                                                               : ATTN_ECUDA;
 #else

@@ -28,8 +28,10 @@ __device__ __forceinline__ void report_status(int code) {
 __device__ unsigned long long g_attn_tiles[3];
 
 #ifdef ATTN_DEBUG_HOOKS
-// Watchdog test build only: a load the forward's TMA warp withholds (0 = none,
-// 1 = the first V tile), so that a consumer's bounded wait runs out.
+// Watchdog test build only: what is withheld, so that a bounded wait for it runs
+// out (0 = nothing, 1 = the first V tile's load by the forward's TMA warp, 2 and
+// 3 = the output head's backward does not count the first vocabulary tile's dz,
+// or the first piece's dx, as finished).
 __device__ int g_attn_withhold;
 #endif
 

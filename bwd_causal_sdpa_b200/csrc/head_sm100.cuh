@@ -852,6 +852,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         bulk_wait_group0();
         if (owed) {
           fence_proxy_async();
+#ifdef ATTN_DEBUG_HOOKS
+          if (!(g_attn_withhold == 2 && owed == dz_done) && !(g_attn_withhold == 3 && owed == dx_done))
+#endif
           red_release(owed, 1u);
           owed = nullptr;
         }
@@ -1257,6 +1260,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     settle();  // stores complete before the CTA ends
   }
 
+  // Where a wait has run out, loads and products of either CTA may be on their way
+  // into this one's memory still. They take microseconds: 400,000 cycles (0.2 ms)
+  // pass before it is given back.
+  __syncwarp();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < 400000) __nanosleep(1000);
+  }
   tc_fence_before();
   __syncwarp();
   __syncthreads();

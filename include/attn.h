@@ -454,8 +454,11 @@ int attn_exp2_selftest(const float* x, float* y, int n, void* stream);
  * every later attn_fwd / attn_fwd_gqa on the tensor-core path withhold the
  * load of its first value tile, so the waits for it run out: the call
  * completes, leaves o and lse undefined and the status word reports
- * ATTN_ETIMEOUT; what = 0 restores normal loads. Synchronous (device-wide).
- * Returns ATTN_OK, ATTN_EINVAL (what not 0 or 1), ATTN_ECUDA, or
+ * ATTN_ETIMEOUT. what = 2 and 3 do the same to attn_head_ce_bwd and
+ * attn_head_distill_bwd (dx and dw undefined): the first 256 vocabulary rows'
+ * dz, or the first vocabulary piece's sums of dx (with several pieces), are
+ * never counted as finished. what = 0 restores normal calls. Synchronous
+ * (device-wide). Returns ATTN_OK, ATTN_EINVAL (what not 0 to 3), ATTN_ECUDA, or
  * ATTN_EUNSUPPORTED in a library built without the hooks (libattn.so). */
 int attn_debug_withhold(int what);
 
