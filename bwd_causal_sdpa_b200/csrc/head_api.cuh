@@ -3,6 +3,8 @@
 // and the entry points attn_head_* of include/attn.h.
 #pragma once
 
+#include <float.h>
+
 #include <algorithm>
 
 #include "head_rows.cuh"
@@ -188,7 +190,8 @@ int head_check(const HeadCall& c, void* ws, size_t ws_bytes) {
   if (c.K == 0 ? !c.target : (!c.t_idx || !c.t_logit)) return ATTN_EINVAL;
   if (c.bwd ? (!c.lse || !c.dloss || !c.dx || !c.dw) : (!c.loss || !c.lse_out)) return ATTN_EINVAL;
   if (c.N <= 0 || c.V <= 0 || c.C <= 0) return ATTN_EINVAL;
-  if (!(c.tau > 0.f) || !isfinite(c.tau) || !isfinite(1.f / c.tau)) return ATTN_EINVAL;
+  // normal: below, 1 / tau in base 2 overflows
+  if (!(c.tau >= FLT_MIN) || !isfinite(c.tau)) return ATTN_EINVAL;
   if (c.t_dtype != ATTN_BF16 && c.t_dtype != ATTN_F32) return ATTN_EINVAL;
   if (c.dw_dtype != ATTN_BF16 && c.dw_dtype != ATTN_F32) return ATTN_EINVAL;
   if (!head_sizes_ok(c.N, c.V, c.C, c.K)) return ATTN_EUNSUPPORTED;

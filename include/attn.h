@@ -388,8 +388,8 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
  * Results do not depend on atomics: the same call gives the same bits.
  *
  * Sizes: N, V, C >= 1, C a multiple of 8, K at most 1024; N and V at most
- * 2^26, C at most 2^20 (else ATTN_EUNSUPPORTED). temperature is positive and
- * finite. x, w, dx, dw and the workspace 16-byte aligned, the others to their
+ * 2^26, C at most 2^20 (else ATTN_EUNSUPPORTED). temperature is positive, finite
+ * and not subnormal. x, w, dx, dw and the workspace 16-byte aligned, the others to their
  * element. Asynchronous on `stream`, like the attention calls.
  *
  * Workspace: attn_head_workspace_bytes(N, V, C, K, is_bwd) bytes, K = 0 for
