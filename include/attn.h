@@ -389,15 +389,20 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
  *
  * Sizes: N, V, C >= 1, C a multiple of 8, K at most 1024; N and V at most
  * 2^26, C at most 2^20 (else ATTN_EUNSUPPORTED). temperature is positive, finite
- * and not subnormal. x, w, dx, dw and the workspace 16-byte aligned, the others to their
- * element. Asynchronous on `stream`, like the attention calls.
+ * and not subnormal. x, w, dx, dw and the workspace 16-byte aligned, the others
+ * to their element. Asynchronous on `stream`, like the attention calls.
  *
  * Workspace: attn_head_workspace_bytes(N, V, C, K, is_bwd) bytes, K = 0 for
- * attn_head_ce*; 0 for invalid sizes. The backward takes the vocabulary in
- * pieces, so its workspace does not grow with V: at most 3 x 96 MiB for dz up
- * to 21504 rows (3 x 4608 bytes a row beyond, and 1 MiB), plus the kept rows of x and the
- * fp32 sums of dx, and is enough for either type of dw. (A teacher's lists add at most N (8 K + V / 32) bytes.) Pure
- * host function.
+ * attn_head_ce*; 0 for invalid sizes. With N and V rounded up to multiples of
+ * 256 the forward takes at most N V / 16 bytes (8 per row and 128 ids; 300 KiB
+ * where that is more) and N (2 C + 64) + V / 16 more, the kept rows of x and
+ * the counters. The backward takes the vocabulary in pieces, so that what it
+ * holds of dz does not grow with V: at most 3 x 96 MiB up to 21504 rows (3 x
+ * 4608 bytes a row beyond, and 1 MiB), plus N (2 C + 64) + V / 16 bytes and
+ * the fp32 sums of dx (4 N C bytes, 20 MB where that is more). It is enough
+ * for either type of dw. A teacher's lists add at most N (12 K + V / 32 + 32)
+ * bytes to either, and the arrays' alignment at most 8 KiB. Pure host
+ * function.
  */
 size_t attn_head_workspace_bytes(int N, int V, int C, int K, int is_bwd);
 int attn_head_ce(const void* x, const void* w, const int32_t* target, float* loss, float* lse,
