@@ -262,58 +262,58 @@ __device__ __forceinline__ Unit find_unit(const Sched& s, int u) {
   };
   if constexpr (!kBwd) {
     if (u < s.dz(0)) logits(LSE, 0);
-    return o;
-  }
-  for (int p = 0; p < min(2, s.pieces); ++p) {
-    if (u < s.dz(p)) {
-      logits(DZ, p);
-      return o;
-    }
-    u -= s.dz(p);
-  }
-  // groups of whole pieces have one size
-  const int group = s.dw(0) + s.dx(0) + s.dz(0);
-  int p = s.pieces > 3 ? min(u / group, s.pieces - 3) : 0;
-  u -= p * group;
-  for (; p < s.pieces; ++p) {
-    for (int k = 0; k < 2; ++k) {
-      if ((k == 0) == s.dx_first) {
-        if (u < s.dx(p)) {
-          o.kind = DX;
-          o.p = p;
-          const int tiles = s.tm * s.tc;
-          o.split = u / tiles;
-          band_tile(u - o.split * tiles, s.tm, s.tc, kBand, o.tm, o.tn);
-          o.kb0 = o.split * s.kb_per;
-          o.nkb = (min(s.kb_v(p), o.kb0 + s.kb_per) - o.kb0) * s.dx_terms;
-          return o;
-        }
-        u -= s.dx(p);
-      } else {
-        if (u < s.dw(p)) {
-          o.kind = DW;
-          o.p = p;
-          o.nkb = s.kb_n * s.dw_terms;
-          band_tile(u, s.tv(p), s.tc, kBand, o.tm, o.tn);
-          if (s.tile_start) {  // lo of the rows that name this tile
-            const int* at = s.tile_start + p * (s.piece / kTile) + o.tm;
-            const int r0 = at[0], r1 = at[1];
-            if (r0 < r1) {
-              o.kb0 = r0 / kKB;
-              o.nkb += (r1 + kKB - 1) / kKB - o.kb0;
-            }
-          }
-          return o;
-        }
-        u -= s.dw(p);
-      }
-    }
-    if (p + 2 < s.pieces) {
-      if (u < s.dz(p + 2)) {
-        logits(DZ, p + 2);
+  } else {
+    for (int p = 0; p < min(2, s.pieces); ++p) {
+      if (u < s.dz(p)) {
+        logits(DZ, p);
         return o;
       }
-      u -= s.dz(p + 2);
+      u -= s.dz(p);
+    }
+    // groups of whole pieces have one size
+    const int group = s.dw(0) + s.dx(0) + s.dz(0);
+    int p = s.pieces > 3 ? min(u / group, s.pieces - 3) : 0;
+    u -= p * group;
+    for (; p < s.pieces; ++p) {
+      for (int k = 0; k < 2; ++k) {
+        if ((k == 0) == s.dx_first) {
+          if (u < s.dx(p)) {
+            o.kind = DX;
+            o.p = p;
+            const int tiles = s.tm * s.tc;
+            o.split = u / tiles;
+            band_tile(u - o.split * tiles, s.tm, s.tc, kBand, o.tm, o.tn);
+            o.kb0 = o.split * s.kb_per;
+            o.nkb = (min(s.kb_v(p), o.kb0 + s.kb_per) - o.kb0) * s.dx_terms;
+            return o;
+          }
+          u -= s.dx(p);
+        } else {
+          if (u < s.dw(p)) {
+            o.kind = DW;
+            o.p = p;
+            o.nkb = s.kb_n * s.dw_terms;
+            band_tile(u, s.tv(p), s.tc, kBand, o.tm, o.tn);
+            if (s.tile_start) {  // lo of the rows that name this tile
+              const int* at = s.tile_start + p * (s.piece / kTile) + o.tm;
+              const int r0 = at[0], r1 = at[1];
+              if (r0 < r1) {
+                o.kb0 = r0 / kKB;
+                o.nkb += (r1 + kKB - 1) / kKB - o.kb0;
+              }
+            }
+            return o;
+          }
+          u -= s.dw(p);
+        }
+      }
+      if (p + 2 < s.pieces) {
+        if (u < s.dz(p + 2)) {
+          logits(DZ, p + 2);
+          return o;
+        }
+        u -= s.dz(p + 2);
+      }
     }
   }
   return o;
