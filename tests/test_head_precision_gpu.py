@@ -111,3 +111,42 @@ def test_few_rows_hold_two_terms(N, left_out, K):
                                             (1100, 3001, 200, 0.3), (1500, 130, 64, 0.0)])
 def test_foremost_entries_of_many_rows_hold_two_terms(N, V, C, left_out, K):
     _check(_workload(N, K, V=V, C=C, left_out=left_out), False, False)
+
+
+@pytest.mark.parametrize("K", [0, 1, 4])
+def test_named_logits_are_rounded_sums(K):
+    """z[target] = -45 as a sum of 2048 products of one sign, every other logit 0:
+    loss = log(V - 1) + 45 up to e^-45 (and less the teacher's entropy). The library sums the few named logits in
+    16 plain fp32 sums of 128 products; what an addition rounds off is spread over
+    half a step either way. Its root mean square over all 2048 is at most
+    sqrt(2048) 2^-22 / sqrt(12) (partial sums stay below 45 / 16 < 4): six times
+    that, half a step (2^-19) for each of the 15 sums that join them at most, of
+    which all but 7 are below 16 (2^-20, 2^-21: 2^-16 in all), and 2^-22 of the
+    loss for the rest. A tensor core cuts the 128 partial sums of such a logit,
+    each by up to a whole step in the same direction, 1.3e-4 on average."""
+    from bwd_causal_sdpa_b200 import ATTN_OK
+    from bwd_causal_sdpa_b200.runner import HeadRunner
+    from workloads import round_to_bf16
+
+    w = make_head_workload(head_config_by_name(CONFIG[min(K, 1)]), N=24, V=300, C=2048, K=K, tau=1.0,
+                           left_out=0.0, ragged=False, seed=77)
+    rng = np.random.default_rng(78)
+    w.x[:] = round_to_bf16((1 + rng.random(w.x.shape)).astype(np.float32))
+    w.w[:] = 0.0
+    w.w[7] = round_to_bf16((-(1 + rng.random(2048)) * 20 / 2048).astype(np.float32))
+    if K:
+        w.t_idx[:] = 7  # the same id K times, each with a share of its own
+    else:
+        w.target[:] = 7
+    z = w.x.astype(np.float64) @ w.w[7].astype(np.float64)
+    assert (-64 < z).all() and (z < -32).all()
+    r = HeadRunner(w)
+    r.forward()
+    assert r.status() == ATTN_OK
+    want = np.log(299 + np.exp(z)) - z
+    if K:
+        _, q = teacher_lists(w.t_idx, w.t_logit, 300, 1.0)
+        want += (q * np.log(q)).sum(axis=1)
+    bound = 6 * np.sqrt(2048 / 12) * 2.0**-22 + 2.0**-16 + 2.0**-22 * want
+    off = np.abs(r.results()["loss"] - want)
+    assert (off <= bound).all(), (off.max(), bound.min())
