@@ -35,8 +35,8 @@
 // rows by the vocabulary tile of that id, so blocks of 64 rows meet the tiles
 // they name along a staircase: at most (rows / 64 + tiles) blocks of lo exist,
 // of rows / 64 x tiles, and they are all that is stored and multiplied. 8192
-// rows of width 768: 0.99 of 0.97 ms, with the sort and the gather of x; all of
-// lo would take a third more.
+// rows of width 768: 0.96 ms before, 0.98 with lo, the sort and the gather of x;
+// all of lo (an fp32 dW) takes 36 % more.
 //
 // Rows whose target is absent (or whose upstream gradients are both zero) are
 // left out: the kept rows are compacted first, so the products cost what the
@@ -56,11 +56,11 @@
 //
 // What bounds it: the tensor cores, and under a steady load the power limit.
 // At 8192 rows, width 2048, 32063 ids the forward's products fill 95 % of the
-// tensor cores' cycles (0.745 ms, 1440 TFLOP/s with the clock down to 1.37 GHz),
-// the backward's 94 % (2.55 ms, 1270 TFLOP/s at 1.25-1.3 GHz); at width 768,
-// where a logits tile is 12 stages long and its epilogue nearly as long, 91 %
-// and 81 % (0.297 and 1.05 ms). The same products by cuBLAS, logits stored:
-// 0.81 and 2.33 ms, 0.36 and 0.98 ms.
+// tensor cores' cycles (0.77 ms, 1395 TFLOP/s with the clock down to 1.37 GHz),
+// and the backward takes 2.67 to 2.74 ms (1180 to 1210 TFLOP/s at 1.25-1.3 GHz);
+// at width 768, where a logits tile is 12 stages long and its epilogue nearly as
+// long, they fill 91 % and 79 % (0.303 and 1.11 ms). The same products by cuBLAS
+// on the same box, logits stored: 0.84 and 2.46 to 2.50 ms, 0.37 and 1.05 ms.
 #pragma once
 
 #include <limits.h>

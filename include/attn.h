@@ -378,8 +378,8 @@ int attn_out_proj_bwd(const void* dy, const void* o, const void* w_o, void* d_o,
  * temperature. dz goes to its two products in bf16, the tensor cores' operand
  * type: in one term (2^-8 relative at most, half a step, beside the output's own
  * rounding) or in two (2^-16).
- *   dw: two terms in fp32 (a third more products), and in bf16 where at most 256
- *       rows are kept; with more of them two terms for the foremost entry of a
+ *   dw: two terms in fp32 (a third more products, two thirds where dx takes them
+ *       too), and in bf16 where at most 256 rows are kept; with more of them two terms for the foremost entry of a
  *       row (its target, or the teacher's largest share, the lowest such id),
  *       the one that outweighs the others (V at most 2^20, else one term);
  *   dx: one term, and in fp32 what the rounding takes from up to four named
