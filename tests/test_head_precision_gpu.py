@@ -49,6 +49,7 @@ def _check(w, dw_f32, all_terms):
     c = w.cfg
     r = HeadRunner(w, dw_dtype=ATTN_F32 if dw_f32 else ATTN_BF16)
     r.forward()
+    r.ws.fill_(0xFF)  # NaN: what the call has not written shows
     r.backward()
     assert r.status() == ATTN_OK
     got = r.results()
@@ -108,7 +109,10 @@ def test_few_rows_hold_two_terms(N, left_out, K):
 
 @pytest.mark.parametrize("K", [0, 1, 3, 30])
 @pytest.mark.parametrize("N,V,C,left_out", [(257, 5000, 72, 0.0), (700, 6000, 72, 0.0),
-                                            (1100, 3001, 200, 0.3), (1500, 130, 64, 0.0)])
+                                            (1100, 3001, 200, 0.3), (1500, 130, 64, 0.0),
+                                            # narrow logits tiles, the last vocabulary tile half empty
+                                            (600, 100, 64, 0.0), (450, 880, 72, 0.2),
+                                            (2000, 1, 8, 0.0), (4099, 20000, 8, 0.9)])
 def test_foremost_entries_of_many_rows_hold_two_terms(N, V, C, left_out, K):
     _check(_workload(N, K, V=V, C=C, left_out=left_out), False, False)
 
